@@ -167,6 +167,96 @@ pf_status pf_text_attn_step(pf_ctx* ctx, int layer, const void* q_txt, const voi
 pf_status pf_qk_rmsnorm(void* x, int64_t n_vectors, int head_dim, const void* gain, float eps,
                         void* stream);
 
+/* Element types of the operators below. */
+typedef enum { PF_BF16 = 0, PF_F16 = 1, PF_F32 = 2 } pf_dtype;
+
+/* Layer normalisation of `groups * rows_per_group` contiguous rows of `channels` elements, with
+ * one (weight, bias) row per group -- one group for an ordinary affine norm, one per sample for
+ * the (scale, shift) modulation of a diffusion transformer (then weight_offset = 1):
+ *   x^ = (x - mean) / sqrt(var + eps),  y = x^ (weight_g + weight_offset) + bias_g
+ * with the statistics in fp32 and one rounding to the type of x.
+ *   x, y       : device, `dtype`; y may be x (in place) but not overlap it otherwise
+ *   weight     : device, `wdtype` (the type of x, or PF_F32), group g's row at
+ *                weight + g * weight_stride elements; NULL for a factor of 1 (no offset)
+ *   bias       : as weight, rows bias_stride apart; NULL for none
+ *   mean, rstd : device fp32 [rows], written for the backward pass; either may be NULL
+ * channels is at most 16384.  Rows that all start on 16-byte boundaries (parameters included)
+ * move in 16-byte accesses; others are allowed and slower.  Pointers must be aligned to their
+ * element (else PF_ERR_ALIGN).  rows_per_group = 0 does nothing. */
+pf_status pf_layernorm(const void* x, void* y, int64_t groups, int64_t rows_per_group,
+                       int channels, const void* weight, int64_t weight_stride,
+                       const void* bias, int64_t bias_stride, float weight_offset, float eps, int dtype, int wdtype, float* mean,
+                       float* rstd, void* stream);
+
+/* Workspace bytes of pf_layernorm_bwd when it returns weight gradients (0 on invalid sizes, or
+ * if there are no rows). */
+size_t pf_layernorm_bwd_workspace_bytes(int64_t groups, int64_t rows_per_group, int channels);
+
+/* Gradients of pf_layernorm.  x, dy, dx: [rows, channels] of `dtype` (dx may be dy or x); weight
+ * and weight_offset as in the forward call, mean and rstd as it wrote them.
+ *   dweight, dbias : device [groups, channels] contiguous, `wdtype`, sums over the group's rows in
+ *                    fp32 in a fixed order (equal inputs give equal bits); either may be NULL
+ *   workspace      : 16-byte aligned device scratch, no initialisation needed, one per
+ *                    concurrently running call; NULL if both sums are NULL */
+pf_status pf_layernorm_bwd(const void* dy, const void* x, int64_t groups, int64_t rows_per_group,
+                           int channels, const void* weight, int64_t weight_stride,
+                           float weight_offset, int dtype, int wdtype, const float* mean,
+                           const float* rstd, void* dx, void* dweight, void* dbias,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Element strides of a [batch, tokens, heads, head_dim] tensor whose head vectors are
+ * contiguous (a view into a packed QKV projection, for instance). */
+typedef struct {
+  int64_t batch, token, head;
+} pf_strides;
+
+/* Rotary embedding over several position axes, after an optional per-head RMS norm.  The head
+ * vector is cut into n_axes sections of axis_dim[a] elements (even; their sum at most head_dim,
+ * the rest is copied); pair i of section a turns by pos[token][a] * theta[a]^(-2 i / axis_dim[a]).
+ *   interleaved = 1: pair i is elements (2 i, 2 i + 1) of its section
+ *   interleaved = 0: pair i is elements (i, i + axis_dim[a] / 2)
+ *   eps = 0: no norm; eps > 0: x / sqrt(mean(x^2) + eps) * gain first
+ * head_dim is a multiple of 8, at most 256.  Angles are reduced in fp64. */
+typedef struct {
+  int batch, tokens; /* >= 0; 0 tokens or batch elements: nothing to do */
+  int heads_q;       /* >= 0, as heads_k; not both 0 */
+  int heads_k;
+  int head_dim;
+  int n_axes; /* 1 .. 4 */
+  int axis_dim[4];
+  double theta[4];
+  int interleaved;
+  int dtype;
+  float eps;
+  int64_t pos_batch_stride; /* floats between batch elements' positions; 0: shared */
+} pf_rope_config;
+
+/* q and k in one launch.  pos: device fp32 [tokens, n_axes] (per batch element
+ * pos_batch_stride apart).  gain_q, gain_k: device [head_dim] of `dtype`, or NULL for 1; only with
+ * eps > 0.  q_out / k_out may be q / k with the same strides (in place).  All pointers (but pos)
+ * and strides are 16-byte multiples.  q, q_out and gain_q are NULL when heads_q is 0; so for k. */
+pf_status pf_qk_norm_rope(const pf_rope_config* cfg, const float* pos, const void* q,
+                          const pf_strides* q_st, const void* k, const pf_strides* k_st,
+                          const void* gain_q, const void* gain_k, void* q_out,
+                          const pf_strides* q_out_st, void* k_out, const pf_strides* k_out_st,
+                          void* stream);
+
+/* Workspace bytes of pf_qk_norm_rope_bwd when it returns gain gradients (0 if cfg is invalid or
+ * there are no tokens). */
+size_t pf_qk_norm_rope_bwd_workspace_bytes(const pf_rope_config* cfg);
+
+/* Gradients of pf_qk_norm_rope: dq_out, dk_out (gradients of its outputs) to dq, dk (of its inputs),
+ * and of the gains (device [head_dim] of `dtype`, or NULL; summed in fp32 in a fixed order).
+ * q and k are the forward inputs; without a norm they are not read and may be NULL.
+ * dq may be dq_out with the same strides.  workspace as in pf_layernorm_bwd. */
+pf_status pf_qk_norm_rope_bwd(const pf_rope_config* cfg, const float* pos, const void* dq_out,
+                              const pf_strides* dq_out_st, const void* dk_out,
+                              const pf_strides* dk_out_st, const void* q, const pf_strides* q_st,
+                              const void* k, const pf_strides* k_st, const void* gain_q,
+                              const void* gain_k, void* dq, const pf_strides* dq_st, void* dk,
+                              const pf_strides* dk_st, void* dgain_q, void* dgain_k,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Bytes of the optional attention workspace for this configuration (0 if cfg is invalid, or
  * if no call of the configuration would split).  With a workspace set, a call may split each
  * query tile's key range over several CTAs so that the grid fills the GPU's SMs in near-whole

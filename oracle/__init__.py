@@ -10,6 +10,7 @@ Modules
 attention   plain-definition patch attention (which rows are fresh, which are stale),
             a stateful KV-buffer walk, and the full-attention primitive.
 cfg         guidance combine eps_u + w (eps_c - eps_u) and rel-MAE_t.
+block       layer norm, QK norm + rotary, attention over masked scores, and their gradients.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py`` against
 closed forms, brute force, reductions to ordinary attention and hand-derived golden

@@ -39,7 +39,13 @@ EXPORTED = [
     "pf_cfg_workspace_bytes", "pf_cfg_combine_relmae", "pf_cfg_combine_relmae_static",
     "pf_check_device_status", "pf_selftest_bounded_wait", "pf_status_string", "pf_version", "pf_switch_init",
     "pf_switch_update", "pf_text_attn_step", "pf_qk_rmsnorm", "pf_get_read_half",
+    "pf_layernorm", "pf_layernorm_bwd", "pf_layernorm_bwd_workspace_bytes", "pf_qk_norm_rope",
+    "pf_qk_norm_rope_bwd", "pf_qk_norm_rope_bwd_workspace_bytes",
 ]
+
+PF_BF16 = 0
+PF_F16 = 1
+PF_F32 = 2
 
 PF_PHASE_WARMUP = 0
 PF_PHASE_PARALLEL = 1
@@ -63,6 +69,19 @@ class pf_switch(ctypes.Structure):
     ]
 
 
+class pf_strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class pf_rope_config(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("heads_q", ctypes.c_int),
+        ("heads_k", ctypes.c_int), ("head_dim", ctypes.c_int), ("n_axes", ctypes.c_int),
+        ("axis_dim", ctypes.c_int * 4), ("theta", ctypes.c_double * 4), ("interleaved", ctypes.c_int),
+        ("dtype", ctypes.c_int), ("eps", ctypes.c_float), ("pos_batch_stride", ctypes.c_int64),
+    ]
+
+
 class PatchAttnError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -81,6 +100,7 @@ def _lib():
         L = ctypes.CDLL(LIB_PATH)
         vp, sz, i, i64, f = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64, ctypes.c_float
         cfgp = ctypes.POINTER(pf_config)
+        stp = ctypes.POINTER(pf_strides)
         sig = {
             "pf_kvbuf_bytes": (sz, [cfgp]),
             "pf_create": (i, [cfgp, ctypes.POINTER(vp), ctypes.POINTER(vp)]),
@@ -103,6 +123,13 @@ def _lib():
             "pf_switch_init": (i, [ctypes.POINTER(pf_switch), f, i, f, i]),
             "pf_switch_update": (i, [ctypes.POINTER(pf_switch), f, ctypes.POINTER(i)]),
             "pf_version": (i, []),
+            "pf_layernorm": (i, [vp, vp, i64, i64, i, vp, i64, vp, i64, f, f, i, i, vp, vp, vp]),
+            "pf_layernorm_bwd": (i, [vp, vp, i64, i64, i, vp, i64, f, i, i, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "pf_layernorm_bwd_workspace_bytes": (sz, [i64, i64, i]),
+            "pf_qk_norm_rope": (i, [ctypes.POINTER(pf_rope_config)] + [vp, vp, stp, vp, stp, vp, vp, vp, stp, vp, stp, vp]),
+            "pf_qk_norm_rope_bwd": (i, [ctypes.POINTER(pf_rope_config), vp] + [vp, stp] * 4 + [vp, vp, vp, stp, vp, stp,
+                                        vp, vp, vp, sz, vp]),
+            "pf_qk_norm_rope_bwd_workspace_bytes": (sz, [ctypes.POINTER(pf_rope_config)]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -410,3 +437,9 @@ def cfg_combine_relmae(eps_c: torch.Tensor, eps_u: torch.Tensor, w: float, want_
     ws = torch.empty(max(16, pf_cfg_workspace_bytes(B, n)), dtype=torch.uint8, device=eps_c.device)
     pf_cfg_combine_relmae(eps_c, eps_u, w, out_f, out_b, rel, ws, stream)
     return out_f, out_b, rel
+
+
+from .block import (  # noqa: E402  (needs the names above)
+    RopeAxes, layernorm, layernorm_backward, pf_layernorm, pf_layernorm_bwd,
+    pf_layernorm_bwd_workspace_bytes, pf_qk_norm_rope, pf_qk_norm_rope_bwd,
+    pf_qk_norm_rope_bwd_workspace_bytes, qk_norm_rope, qk_norm_rope_backward)

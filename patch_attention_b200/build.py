@@ -12,6 +12,7 @@ import argparse
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,8 +21,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpatchattn.so")
 OBJDIR = os.path.join(HERE, "_build")
 
-SOURCES = ["attn_fwd.cu", "cfg_combine.cu", "kvbuf_copy.cu", "qk_rmsnorm.cu", "pf_api.cpp"]
-HEADERS = ["pf_internal.h", "sm100_ptx.cuh"]
+SOURCES = ["attn_fwd.cu", "cfg_combine.cu", "kvbuf_copy.cu", "qk_rmsnorm.cu", "layernorm.cu",
+           "qk_norm_rope.cu", "pf_api.cpp", "pf_block_api.cpp"]
+HEADERS = ["pf_internal.h", "sm100_ptx.cuh", "block_ops.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -43,7 +45,7 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,
     extra = ["-DPF_TRACE"] if trace else []
     os.makedirs(objdir, exist_ok=True)
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "patchattn.h")]
-    objs = []
+    objs, todo = [], []
     for src in SOURCES:
         path = os.path.join(CSRC, src)
         obj = os.path.join(objdir, src + ".o")
@@ -54,11 +56,14 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,
                 cmd += ["-Xptxas", "-v"]
             if src.endswith(".cpp"):
                 cmd = [NVCC] + ARCH + COMMON + ["-x", "c++", "-c", path, "-o", obj]
-            r = subprocess.run(cmd, capture_output=True, text=True)
-            if r.returncode != 0 or not quiet:
-                sys.stderr.write(r.stdout + r.stderr)
-            if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed on {src}")
+            todo.append((src, cmd))
+    with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+        done = list(pool.map(lambda t: subprocess.run(t[1], capture_output=True, text=True), todo))
+    for (src, _), r in zip(todo, done):
+        if r.returncode != 0 or not quiet:
+            sys.stderr.write(r.stdout + r.stderr)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc failed on {src}")
     if force or _stale(lib, objs):
         cmd = [NVCC] + ARCH + ["-shared", "-cudart", "static", "-o", lib] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)

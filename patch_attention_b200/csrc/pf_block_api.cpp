@@ -1,0 +1,223 @@
+// pf_block_api.cpp -- host side of the transformer-block operators declared in
+// include/patchattn.h: layer norm, QK norm + rotary, and their gradients.  Checks every
+// argument before anything is enqueued; holds no state.
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "patchattn.h"
+#include "pf_internal.h"
+
+namespace {
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool dtype_ok(int t) { return t == PF_BF16 || t == PF_F16 || t == PF_F32; }
+size_t elem_bytes(int t) { return t == PF_F32 ? 4 : 2; }
+pf_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PF_OK : PF_ERR_CUDA; }
+
+// Sizes every layer-norm call checks: launch grids and row counts fit 31 bits.
+pf_status check_ln_sizes(int64_t groups, int64_t rows_per_group, int channels) {
+  if (groups < 1 || rows_per_group < 0 || channels < 1 || channels > pf::kLnMaxChannels) return PF_ERR_SHAPE;
+  if (groups > INT32_MAX || rows_per_group > INT32_MAX || groups * rows_per_group > INT32_MAX) return PF_ERR_SHAPE;
+  if (groups * 2 * ((channels + 31) / 32) > INT32_MAX) return PF_ERR_SHAPE;
+  return PF_OK;
+}
+
+pf_status check_ln(const pf::LnArgs& a) {
+  const pf_status st = check_ln_sizes(a.groups, a.rows_per_group, a.channels);
+  if (st != PF_OK) return st;
+  if (!dtype_ok(a.dtype) || (a.wdtype != a.dtype && a.wdtype != PF_F32)) return PF_ERR_UNSUPPORTED;
+  if (!std::isfinite(a.weight_offset)) return PF_ERR_INVALID_ARG;
+  if (a.groups > 1 && ((a.weight && a.weight_stride < a.channels) || (a.bias && a.bias_stride < a.channels)))
+    return PF_ERR_INVALID_ARG;
+  const size_t e = elem_bytes(a.dtype), we = elem_bytes(a.wdtype);
+  if (!aligned(a.x, e) || !aligned(a.dy, e) || !aligned(a.y, e) || !aligned(a.weight, we) || !aligned(a.bias, we) ||
+      !aligned(a.mean, 4) || !aligned(a.rstd, 4))
+    return PF_ERR_ALIGN;
+  return PF_OK;
+}
+
+// The pairs of a head vector, section by section; the rest of the vector is a section that
+// does not turn.
+pf_status make_rope(const pf_rope_config* c, pf::RopeArgs& a) {
+  if (!c) return PF_ERR_INVALID_ARG;
+  if (c->batch < 0 || c->tokens < 0 || c->heads_q < 0 || c->heads_k < 0 || c->heads_q + c->heads_k < 1 ||
+      c->heads_q > 65536 || c->heads_k > 65536)
+    return PF_ERR_SHAPE;
+  if (c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8 != 0) return PF_ERR_SHAPE;
+  if (c->n_axes < 1 || c->n_axes > 4) return PF_ERR_SHAPE;
+  if (!dtype_ok(c->dtype)) return PF_ERR_UNSUPPORTED;
+  if (!(c->eps >= 0.f) || std::isinf(c->eps)) return PF_ERR_INVALID_ARG;
+  if (c->pos_batch_stride < 0) return PF_ERR_INVALID_ARG;
+  // items (tokens times head shares) are counted in blocks of 8 warps on a 31-bit grid
+  if (static_cast<int64_t>(c->batch) * c->tokens > INT32_MAX) return PF_ERR_SHAPE;
+  std::memset(&a, 0, sizeof(a));
+  a.batch = c->batch;
+  a.tokens = c->tokens;
+  a.n_axes = c->n_axes;
+  a.heads[0] = c->heads_q;
+  a.heads[1] = c->heads_k;
+  a.head_dim = c->head_dim;
+  a.dtype = c->dtype;
+  a.interleaved = c->interleaved != 0;
+  a.eps = c->eps;
+  a.pos_batch = c->pos_batch_stride;
+  int base = 0, pair = 0, half_bits = 4;
+  for (int ax = 0; ax <= c->n_axes; ++ax) {
+    const bool rest = ax == c->n_axes;
+    const int w = rest ? c->head_dim - base : c->axis_dim[ax];
+    if (w < 0 || w % 2 != 0 || (!rest && w == 0) || base + w > c->head_dim) return PF_ERR_SHAPE;
+    if (!rest && (!(c->theta[ax] > 0.0) || std::isinf(c->theta[ax]))) return PF_ERR_INVALID_ARG;
+    for (int i = 0; i < w / 2; ++i, ++pair) {
+      a.tab.axis[pair] = static_cast<uint8_t>(ax);
+      a.tab.e0[pair] = static_cast<uint8_t>(base + (a.interleaved ? 2 * i : i));
+      a.tab.e1[pair] = static_cast<uint8_t>(base + (a.interleaved ? 2 * i + 1 : i + w / 2));
+      a.tab.turns[pair] = rest ? 0.0 : std::pow(c->theta[ax], -2.0 * i / w) / 6.283185307179586476925;
+    }
+    half_bits |= w / 2;
+    base += w;
+  }
+  a.tab.half_align = half_bits & -half_bits;
+  return PF_OK;
+}
+
+// One operand of a rotary call: present exactly when it has heads, 16-byte aligned throughout.
+pf_status take_operand(const pf::RopeArgs& a, int which, const void* p, const pf_strides* st, bool needed,
+                       const void** out, long long (*strides)[3]) {
+  *out = nullptr;
+  if (a.heads[which] == 0) return p == nullptr ? PF_OK : PF_ERR_INVALID_ARG;
+  if (!needed) return PF_OK;
+  if (a.batch == 0 || a.tokens == 0) return PF_OK;
+  if (!p || !st) return PF_ERR_INVALID_ARG;
+  const int64_t unit = 16 / static_cast<int64_t>(elem_bytes(a.dtype));
+  if (!aligned(p, 16) || st->batch % unit != 0 || st->token % unit != 0 || st->head % unit != 0) return PF_ERR_ALIGN;
+  *out = p;
+  strides[which][0] = st->batch;
+  strides[which][1] = st->token;
+  strides[which][2] = st->head;
+  return PF_OK;
+}
+
+pf_status take_gain(pf::RopeArgs& a, int which, const void* g) {
+  if (!g) return PF_OK;
+  if (a.eps == 0.f || a.heads[which] == 0) return PF_ERR_INVALID_ARG;
+  if (!aligned(g, 16)) return PF_ERR_ALIGN;
+  a.gain[which] = g;
+  return PF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pf_status pf_layernorm(const void* x, void* y, int64_t groups, int64_t rows_per_group, int channels,
+                       const void* weight, int64_t weight_stride, const void* bias, int64_t bias_stride,
+                       float weight_offset, float eps, int dtype, int wdtype, float* mean, float* rstd, void* stream) {
+  pf::LnArgs a = {x, nullptr, y, weight, bias, mean, rstd, groups, rows_per_group, weight_stride,
+                  bias_stride, channels, dtype, wdtype, weight_offset, eps};
+  const pf_status st = check_ln(a);
+  if (st != PF_OK) return st;
+  if (!(eps > 0.f) || std::isinf(eps)) return PF_ERR_INVALID_ARG;
+  if (rows_per_group == 0) return PF_OK;
+  if (!x || !y) return PF_ERR_INVALID_ARG;
+  return from_cuda(pf::launch_layernorm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pf_layernorm_bwd_workspace_bytes(int64_t groups, int64_t rows_per_group, int channels) {
+  if (check_ln_sizes(groups, rows_per_group, channels) != PF_OK || rows_per_group == 0) return 0;
+  return static_cast<size_t>(groups) * pf::ln_bwd_parts(groups, rows_per_group) * 2 * channels * 4;
+}
+
+pf_status pf_layernorm_bwd(const void* dy, const void* x, int64_t groups, int64_t rows_per_group, int channels,
+                           const void* weight, int64_t weight_stride, float weight_offset, int dtype, int wdtype,
+                           const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  pf::LnArgs a = {x, dy, dx, weight, nullptr, const_cast<float*>(mean), const_cast<float*>(rstd), groups,
+                  rows_per_group, weight_stride, 0, channels, dtype, wdtype, weight_offset, 0.f};
+  const pf_status st = check_ln(a);
+  if (st != PF_OK) return st;
+  if (rows_per_group > 0 && (!dy || !x || !dx || !mean || !rstd)) return PF_ERR_INVALID_ARG;
+  const size_t we = elem_bytes(wdtype);
+  if (!aligned(dweight, we) || !aligned(dbias, we) || !aligned(workspace, 16)) return PF_ERR_ALIGN;
+  if (dweight || dbias) {
+    const size_t need = pf_layernorm_bwd_workspace_bytes(groups, rows_per_group, channels);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return PF_ERR_INVALID_ARG;
+  }
+  return from_cuda(pf::launch_layernorm_bwd(a, dweight, dbias, static_cast<float*>(workspace),
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+pf_status pf_qk_norm_rope(const pf_rope_config* cfg, const float* pos, const void* q, const pf_strides* q_st,
+                          const void* k, const pf_strides* k_st, const void* gain_q, const void* gain_k,
+                          void* q_out, const pf_strides* q_out_st, void* k_out, const pf_strides* k_out_st,
+                          void* stream) {
+  pf::RopeArgs a;
+  pf_status st = make_rope(cfg, a);
+  const void* in[2] = {q, k};
+  const pf_strides* in_st[2] = {q_st, k_st};
+  const void* out[2] = {q_out, k_out};
+  const pf_strides* out_st[2] = {q_out_st, k_out_st};
+  const void* gain[2] = {gain_q, gain_k};
+  for (int w = 0; w < 2 && st == PF_OK; ++w) {
+    const void* y = nullptr;
+    st = take_operand(a, w, in[w], in_st[w], true, &a.x[w], a.xs);
+    if (st == PF_OK) st = take_operand(a, w, out[w], out_st[w], true, &y, a.ys);
+    a.y[w] = const_cast<void*>(y);
+    if (st == PF_OK) st = take_gain(a, w, gain[w]);
+  }
+  if (st != PF_OK) return st;
+  if (a.batch == 0 || a.tokens == 0) return PF_OK;
+  if (!pos) return PF_ERR_INVALID_ARG;
+  if (!aligned(pos, 4)) return PF_ERR_ALIGN;
+  a.pos = pos;
+  return from_cuda(pf::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pf_qk_norm_rope_bwd_workspace_bytes(const pf_rope_config* cfg) {
+  pf::RopeArgs a;
+  if (make_rope(cfg, a) != PF_OK) return 0;
+  return static_cast<size_t>(pf::rope_bwd_blocks(a)) * 2 * a.head_dim * 4;
+}
+
+pf_status pf_qk_norm_rope_bwd(const pf_rope_config* cfg, const float* pos, const void* dq_out,
+                              const pf_strides* dq_out_st, const void* dk_out, const pf_strides* dk_out_st,
+                              const void* q, const pf_strides* q_st, const void* k, const pf_strides* k_st,
+                              const void* gain_q, const void* gain_k, void* dq, const pf_strides* dq_st, void* dk,
+                              const pf_strides* dk_st, void* dgain_q, void* dgain_k, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  pf::RopeArgs a;
+  pf_status st = make_rope(cfg, a);
+  const void* up[2] = {dq_out, dk_out};
+  const pf_strides* up_st[2] = {dq_out_st, dk_out_st};
+  const void* in[2] = {q, k};
+  const pf_strides* in_st[2] = {q_st, k_st};
+  const void* out[2] = {dq, dk};
+  const pf_strides* out_st[2] = {dq_st, dk_st};
+  const void* gain[2] = {gain_q, gain_k};
+  const void* dgain[2] = {dgain_q, dgain_k};
+  for (int w = 0; w < 2 && st == PF_OK; ++w) {
+    const void* y = nullptr;
+    st = take_operand(a, w, up[w], up_st[w], true, &a.dy[w], a.ds);
+    if (st == PF_OK) st = take_operand(a, w, in[w], in_st[w], a.eps > 0.f, &a.x[w], a.xs);
+    if (st == PF_OK) st = take_operand(a, w, out[w], out_st[w], true, &y, a.ys);
+    a.y[w] = const_cast<void*>(y);
+    if (st == PF_OK) st = take_gain(a, w, gain[w]);
+    if (st == PF_OK && dgain[w] && (a.eps == 0.f || a.heads[w] == 0)) st = PF_ERR_INVALID_ARG;
+    if (st == PF_OK && !aligned(dgain[w], elem_bytes(a.dtype))) st = PF_ERR_ALIGN;
+  }
+  if (st != PF_OK) return st;
+  if (!aligned(workspace, 16) || !aligned(pos, 4)) return PF_ERR_ALIGN;
+  if (dgain_q || dgain_k) {
+    const size_t need = pf_qk_norm_rope_bwd_workspace_bytes(cfg);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return PF_ERR_INVALID_ARG;
+  }
+  if (a.batch > 0 && a.tokens > 0 && !pos) return PF_ERR_INVALID_ARG;
+  a.pos = pos;
+  return from_cuda(pf::launch_qk_norm_rope_bwd(a, dgain_q, dgain_k, static_cast<float*>(workspace),
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "patchattn.h"
+
 namespace pf {
 
 // Kernel parameters of one patch-attention micro-step.  Tensor maps describe 4-D
@@ -98,6 +100,47 @@ cudaError_t launch_cfg_combine_relmae_static(const float* c, const float* u, int
                                              float w, float* out_f32, uint16_t* out_bf16,
                                              float* relmae, cudaStream_t stream);
 int cfg_static_capacity_samples();
+
+// Layer normalisation, forward (y) and backward (y holds dx).  Checked by the host API.
+struct LnArgs {
+  const void* x;
+  const void* dy;
+  void* y;
+  const void* weight;
+  const void* bias;
+  float* mean;
+  float* rstd;
+  long long groups, rows_per_group, weight_stride, bias_stride;
+  int channels, dtype, wdtype;
+  float weight_offset, eps;
+};
+constexpr int kLnMaxChannels = 16384;
+// Row ranges per group of the backward pass (partial rows of the weight gradient).
+int ln_bwd_parts(long long groups, long long rows_per_group);
+cudaError_t launch_layernorm(const LnArgs& a, cudaStream_t stream);
+cudaError_t launch_layernorm_bwd(const LnArgs& a, void* dweight, void* dbias, float* part, cudaStream_t stream);
+
+// Pairs of a head vector: elements, axis (n_axes: not rotated) and turns per unit position.
+struct RopeTable {
+  double turns[128];
+  uint8_t e0[128], e1[128], axis[128];
+  int half_align;  // greatest power of two (at most 4) dividing every section's half width
+};
+struct RopeArgs {
+  const void* x[2];   // q, k
+  const void* dy[2];
+  void* y[2];
+  const void* gain[2];
+  long long xs[2][3], ds[2][3], ys[2][3];
+  const float* pos;
+  long long pos_batch;
+  int batch, tokens, n_axes, heads[2], head_dim, dtype, interleaved;
+  float eps;
+  RopeTable tab;
+};
+int rope_bwd_blocks(const RopeArgs& a);
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, void* dgain_q, void* dgain_k, float* part, cudaStream_t stream);
 
 // Device word written by kernels whose bounded waits expired (0 = none).
 cudaError_t read_and_clear_watchdog(unsigned* value);
