@@ -257,6 +257,43 @@ pf_status pf_qk_norm_rope_bwd(const pf_rope_config* cfg, const float* pos, const
                               const pf_strides* dk_st, void* dgain_q, void* dgain_k,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/* Attention over capped, biased and masked scores.  Query i stands at position
+ * p_i = i + n_k - n_q (the queries are the last positions), key j at j; with scale = softmax_scale:
+ *   s_ij = scale q_i.k_j;  s_ij <- softcap tanh(s_ij / softcap) if softcap > 0;
+ *   s_ij <- s_ij - slopes[head] |p_i - j| if slopes is given
+ *   key j is visible to query i if (causal = 0, or j <= p_i, or j < prefix[batch] where prefix is
+ *   given) and, where documents are given, doc_q[i] = doc_k[j] >= 0 (a negative id is padding)
+ *   o_i = sum over visible j of softmax_j(s_ij) v_j; a query that sees no key gives 0
+ * Keys and values that no query sees may hold anything (padding, unwritten cache rows); those that
+ * some query sees should be finite, as a value reaches its whole tile of 128 rows. */
+typedef struct {
+  int batch;           /* >= 1 */
+  int heads_q;         /* >= 1, a multiple of heads_kv: query head h uses key head h * heads_kv / heads_q */
+  int heads_kv;
+  int head_dim;        /* 64, 72 or 128 */
+  int n_q, n_k;        /* >= 0, at most 2^30; with documents n_k is at most 2^20 */
+  float softmax_scale; /* 0 => 1/sqrt(head_dim) */
+  float softcap;       /* 0 => none */
+  int causal;
+  pf_strides q, k, v;  /* element strides, positive multiples of 8 (where the extent is above 1) */
+} pf_masked_attn_config;
+
+/*   q, k, v : device bf16, [batch, n_q, heads_q, d] and [batch, n_k, heads_kv, d] by their strides
+ *   slopes  : device fp32 [heads_q] or NULL
+ *   prefix  : device int32 [batch] or NULL; only with causal
+ *   doc_q, doc_k : device int32 [batch, n_q], [batch, n_k], contiguous, or both NULL
+ *   o       : device bf16 [batch, n_q, heads_q, d] contiguous, not overlapping an input
+ *   lse     : device fp32 [batch, heads_q, n_q] or NULL: log of the sum of exp(s) over the visible
+ *             keys (-inf if there are none), for the backward pass
+ * No workspace.  A kernel whose bounded wait expired shows in pf_device_status. */
+pf_status pf_masked_attn(const pf_masked_attn_config* cfg, const void* q, const void* k,
+                         const void* v, const float* slopes, const int32_t* prefix,
+                         const int32_t* doc_q, const int32_t* doc_k, void* o, float* lse,
+                         void* stream);
+
+/* pf_check_device_status for operators that have no context. */
+pf_status pf_device_status(void* stream);
+
 /* Bytes of the optional attention workspace for this configuration (0 if cfg is invalid, or
  * if no call of the configuration would split).  With a workspace set, a call may split each
  * query tile's key range over several CTAs so that the grid fills the GPU's SMs in near-whole

@@ -40,7 +40,7 @@ EXPORTED = [
     "pf_check_device_status", "pf_selftest_bounded_wait", "pf_status_string", "pf_version", "pf_switch_init",
     "pf_switch_update", "pf_text_attn_step", "pf_qk_rmsnorm", "pf_get_read_half",
     "pf_layernorm", "pf_layernorm_bwd", "pf_layernorm_bwd_workspace_bytes", "pf_qk_norm_rope",
-    "pf_qk_norm_rope_bwd", "pf_qk_norm_rope_bwd_workspace_bytes",
+    "pf_qk_norm_rope_bwd", "pf_qk_norm_rope_bwd_workspace_bytes", "pf_masked_attn", "pf_device_status",
 ]
 
 PF_BF16 = 0
@@ -79,6 +79,15 @@ class pf_rope_config(ctypes.Structure):
         ("heads_k", ctypes.c_int), ("head_dim", ctypes.c_int), ("n_axes", ctypes.c_int),
         ("axis_dim", ctypes.c_int * 4), ("theta", ctypes.c_double * 4), ("interleaved", ctypes.c_int),
         ("dtype", ctypes.c_int), ("eps", ctypes.c_float), ("pos_batch_stride", ctypes.c_int64),
+    ]
+
+
+class pf_masked_attn_config(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int), ("heads_q", ctypes.c_int), ("heads_kv", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("n_q", ctypes.c_int), ("n_k", ctypes.c_int),
+        ("softmax_scale", ctypes.c_float), ("softcap", ctypes.c_float), ("causal", ctypes.c_int),
+        ("q", pf_strides), ("k", pf_strides), ("v", pf_strides),
     ]
 
 
@@ -129,6 +138,8 @@ def _lib():
             "pf_qk_norm_rope": (i, [ctypes.POINTER(pf_rope_config)] + [vp, vp, stp, vp, stp, vp, vp, vp, stp, vp, stp, vp]),
             "pf_qk_norm_rope_bwd": (i, [ctypes.POINTER(pf_rope_config), vp] + [vp, stp] * 4 + [vp, vp, vp, stp, vp, stp,
                                         vp, vp, vp, sz, vp]),
+            "pf_masked_attn": (i, [ctypes.POINTER(pf_masked_attn_config)] + [vp] * 10),
+            "pf_device_status": (i, [vp]),
             "pf_qk_norm_rope_bwd_workspace_bytes": (sz, [ctypes.POINTER(pf_rope_config)]),
         }
         for name, (res, args) in sig.items():
@@ -440,6 +451,6 @@ def cfg_combine_relmae(eps_c: torch.Tensor, eps_u: torch.Tensor, w: float, want_
 
 
 from .block import (  # noqa: E402  (needs the names above)
-    RopeAxes, layernorm, layernorm_backward, pf_layernorm, pf_layernorm_bwd,
-    pf_layernorm_bwd_workspace_bytes, pf_qk_norm_rope, pf_qk_norm_rope_bwd,
+    RopeAxes, ScoreRule, layernorm, layernorm_backward, masked_attention, pf_device_status, pf_layernorm,
+    pf_layernorm_bwd, pf_layernorm_bwd_workspace_bytes, pf_masked_attn, pf_qk_norm_rope, pf_qk_norm_rope_bwd,
     pf_qk_norm_rope_bwd_workspace_bytes, qk_norm_rope, qk_norm_rope_backward)

@@ -1,6 +1,6 @@
 """Operators of a diffusion transformer's block around the patch attention: layer norm with an
-affine or a per-sample modulation, and QK norm with a rotary embedding over several position
-axes, each with its gradients.
+affine or a per-sample modulation, QK norm with a rotary embedding over several position axes,
+and attention over capped, biased and masked scores, each with its gradients.
 
 The ``pf_*`` functions carry the C ABI's names (``include/patchattn.h``) and fill tensors that
 the caller allocated; the others allocate their outputs with torch.  All tensors of a call are on
@@ -17,7 +17,7 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from . import (PF_BF16, PF_F16, PF_F32, _check, _lib, pf_rope_config, pf_strides)
+from . import PF_BF16, PF_F16, PF_F32, _check, _lib, pf_masked_attn_config, pf_rope_config, pf_strides
 
 _DTYPES = {torch.bfloat16: PF_BF16, torch.float16: PF_F16, torch.float32: PF_F32}
 _HERE = contextlib.nullcontext()
@@ -320,3 +320,82 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
             ws = torch.empty(nbytes, dtype=torch.uint8, device=lead.device)
         pf_qk_norm_rope_bwd(dq_out, dk_out, q, k, pos, axes, dq, dk, gain_q, gain_k, eps, dgq, dgk, ws)
     return dq, dk, dgq, dgk
+
+
+# ------------------------------------------------------------------ masked attention
+
+
+class ScoreRule:
+    """What attention does to its scores before the softmax: ``softmax_scale`` (0: 1/sqrt(head_dim)), a cap
+    ``softcap * tanh(s / softcap)`` (0: none), a distance bias ``-slopes[head] * |position - key|``, and which keys a
+    query sees: all, or with ``causal`` those up to its position (queries are the last positions) and those before
+    ``prefix[batch]``; and, with ``doc_q`` and ``doc_k`` (int32 ids, negative: padding), only keys of its document."""
+
+    def __init__(self, softmax_scale: float = 0.0, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                 causal: bool = False, prefix: Optional[torch.Tensor] = None, doc_q: Optional[torch.Tensor] = None,
+                 doc_k: Optional[torch.Tensor] = None):
+        if prefix is not None and not causal:
+            raise ValueError("a prefix goes with a causal mask")
+        if (doc_q is None) != (doc_k is None):
+            raise ValueError("doc_q and doc_k come together")
+        self.softmax_scale, self.softcap, self.causal = float(softmax_scale), float(softcap), bool(causal)
+        self.slopes, self.prefix, self.doc_q, self.doc_k = slopes, prefix, doc_q, doc_k
+
+    def tensors(self):
+        return self.slopes, self.prefix, self.doc_q, self.doc_k
+
+
+def _masked_args(q, k, v, rule: ScoreRule):
+    """(configuration, pointers of q, k, v, pointers of the rule's tensors)."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [batch, tokens, heads, head_dim], got {tuple(t.shape)}")
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+    b, nq, hq, d = q.shape
+    nk, hk = k.shape[1], k.shape[2]
+    if tuple(k.shape) != (b, nk, hk, d) or v.shape != k.shape:
+        raise ValueError(f"q, k, v of shapes {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)} do not go together")
+    (qp, qs), (kp, ks), (vp, vs) = _heads_view(q, None, "q"), _heads_view(k, None, "k"), _heads_view(v, None, "v")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _no_overlap(t, name)
+    cfg = pf_masked_attn_config(b, hq, hk, d, nq, nk, rule.softmax_scale, rule.softcap, int(rule.causal), qs, ks, vs)
+    extra = (_whole(rule.slopes, torch.float32, (hq,), "slopes"), _whole(rule.prefix, torch.int32, (b,), "prefix"),
+             _whole(rule.doc_q, torch.int32, (b, nq), "doc_q"), _whole(rule.doc_k, torch.int32, (b, nk), "doc_k"))
+    return cfg, (qp, kp, vp), extra
+
+
+_PLAIN = ScoreRule()
+
+
+def pf_masked_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                   lse: Optional[torch.Tensor] = None, rule: Optional[ScoreRule] = None, stream=None) -> None:
+    rule = rule or _PLAIN
+    dev = _device(q, k, v, o, lse, *rule.tensors())
+    cfg, ptrs, extra = _masked_args(q, k, v, rule)
+    op = _whole(o, torch.bfloat16, q.shape, "o")
+    lp = _whole(lse, torch.float32, (q.shape[0], q.shape[2], q.shape[1]), "lse")
+    with _on(dev, stream):
+        _check(_lib().pf_masked_attn(cfg, *ptrs, *extra, op, lp, _raw_stream(dev)), "pf_masked_attn")
+
+
+def pf_device_status(stream=None) -> None:
+    """Synchronise the stream; raises if a kernel's bounded wait expired on this device."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    _check(_lib().pf_device_status(raw), "pf_device_status")
+
+
+def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rule: Optional[ScoreRule] = None, *,
+                     want_lse: bool = False, stream=None):
+    """Attention of bf16 q [batch, n_q, heads_q, d] over k, v [batch, n_k, heads_kv, d] (views with contiguous head
+    vectors are fine; heads_q a multiple of heads_kv; d in 64, 72, 128) with the scores changed and masked by
+    ``rule``.  Returns o, or (o, lse) with the fp32 [batch, heads_q, n_q] statistics of the backward pass."""
+    with _on(_device(q), stream):
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = None
+        if want_lse:
+            lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
+        pf_masked_attn(q, k, v, o, lse, rule)
+    return (o, lse) if want_lse else o

@@ -1632,6 +1632,10 @@ cudaError_t launch_selftest_wait(uint64_t limit_ns, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+cudaError_t watchdog_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_watchdog);
+}
+
 cudaError_t read_and_clear_watchdog(unsigned* value) {
   unsigned v = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_watchdog, sizeof(v));

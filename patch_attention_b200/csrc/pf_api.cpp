@@ -254,6 +254,21 @@ uint8_t* region(const pf_ctx* ctx, int layer, int half, int kv) {
 }  // namespace
 
 namespace pf {
+bool encode_heads_map(CUtensorMap* m, const void* base, int batch, int rows, int heads, int d, const pf_strides& st,
+                      int box_heads, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
+  auto bytes = [](int64_t s, int extent) { return extent > 1 ? static_cast<cuuint64_t>(s) * 2 : cuuint64_t{16}; };
+  const cuuint64_t strides[3] = {bytes(st.head, heads), bytes(st.token, rows), bytes(st.batch, batch)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t device_is_sm100(bool* ok) {
   int dev = 0, major = 0, minor = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -642,6 +657,13 @@ pf_status pf_switch_update(pf_switch* s, float relmae, int* phase_out) {
 
 pf_status pf_check_device_status(pf_ctx* ctx, void* stream) {
   if (!ctx) return PF_ERR_INVALID_ARG;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return PF_ERR_CUDA;
+  unsigned v = 0;
+  if (pf::read_and_clear_watchdog(&v) != cudaSuccess) return PF_ERR_CUDA;
+  return v ? PF_ERR_TIMEOUT : PF_OK;
+}
+
+pf_status pf_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return PF_ERR_CUDA;
   unsigned v = 0;
   if (pf::read_and_clear_watchdog(&v) != cudaSuccess) return PF_ERR_CUDA;

@@ -1,9 +1,10 @@
 // pf_block_api.cpp -- host side of the transformer-block operators declared in
-// include/patchattn.h: layer norm, QK norm + rotary, and their gradients.  Checks every
+// include/patchattn.h: layer norm, QK norm + rotary, masked attention, and their gradients.  Checks every
 // argument before anything is enqueued; holds no state.
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -108,6 +109,86 @@ pf_status take_gain(pf::RopeArgs& a, int which, const void* g) {
   a.gain[which] = g;
   return PF_OK;
 }
+
+// ------------------------------------------------------------------ masked attention
+
+constexpr int kMaxTokens = 1 << 30;
+
+// Strides of one operand: positive multiples of 16 bytes below 2^40 where the extent is above 1.
+pf_status check_strides(const pf_strides& s, int batch, int rows, int heads) {
+  const int64_t v[3] = {s.batch, s.token, s.head};
+  const int extent[3] = {batch, rows, heads};
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] <= 1) continue;
+    if (v[i] <= 0 || v[i] >= (int64_t{1} << 39)) return PF_ERR_INVALID_ARG;
+    if (v[i] % 8 != 0) return PF_ERR_ALIGN;
+  }
+  return PF_OK;
+}
+
+pf_status check_masked(const pf_masked_attn_config* c) {
+  if (!c) return PF_ERR_INVALID_ARG;
+  if (c->batch < 1 || c->heads_q < 1 || c->heads_kv < 1 || c->heads_q % c->heads_kv != 0) return PF_ERR_SHAPE;
+  if (c->n_q < 0 || c->n_k < 0 || c->n_q > kMaxTokens || c->n_k > kMaxTokens) return PF_ERR_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 72 && c->head_dim != 128) return PF_ERR_UNSUPPORTED;
+  if (!(c->softmax_scale >= 0.f) || std::isinf(c->softmax_scale)) return PF_ERR_INVALID_ARG;
+  if (!(c->softcap >= 0.f) || std::isinf(c->softcap)) return PF_ERR_INVALID_ARG;
+  // CTAs (at most 8 per query tile and head, or per key tile) on a 31-bit grid
+  const double longest = c->n_q > c->n_k ? c->n_q : c->n_k;
+  if (static_cast<double>(c->batch) * c->heads_q * (longest / 128 + 1) * 8 > 2147483647.0) return PF_ERR_SHAPE;
+  pf_status st = check_strides(c->q, c->batch, c->n_q, c->heads_q);
+  if (st == PF_OK) st = check_strides(c->k, c->batch, c->n_k, c->heads_kv);
+  if (st == PF_OK) st = check_strides(c->v, c->batch, c->n_k, c->heads_kv);
+  return st;
+}
+
+pf_status make_mask(const pf_masked_attn_config& c, const float* slopes, const int32_t* prefix, const int32_t* doc_q,
+                    const int32_t* doc_k, pf::MaskParams& m) {
+  if (prefix && !c.causal) return PF_ERR_INVALID_ARG;
+  if ((doc_q != nullptr) != (doc_k != nullptr) && c.n_q > 0 && c.n_k > 0) return PF_ERR_INVALID_ARG;
+  const bool docs = doc_q && doc_k;
+  if (docs && c.n_k > pf::kMaskedDocTiles * 128) return PF_ERR_SHAPE;
+  if (!aligned(slopes, 4) || !aligned(prefix, 4) || !aligned(doc_q, 4) || !aligned(doc_k, 4)) return PF_ERR_ALIGN;
+  const float scale = c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / std::sqrt(static_cast<float>(c.head_dim));
+  const float log2e = 1.4426950408889634f;
+  m.prefix = prefix;
+  m.doc_q = docs ? doc_q : nullptr;
+  m.doc_k = docs ? doc_k : nullptr;
+  m.slopes = slopes;
+  m.causal = c.causal != 0;
+  m.n_q = c.n_q;
+  m.n_k = c.n_k;
+  m.scale_log2 = scale * log2e;
+  m.cap_log2 = c.softcap * log2e;
+  m.cap_in = c.softcap > 0.f ? 2.f * scale / c.softcap * log2e : 0.f;
+  if (!std::isfinite(m.scale_log2) || !std::isfinite(m.cap_log2) || !std::isfinite(m.cap_in)) return PF_ERR_INVALID_ARG;
+  return PF_OK;
+}
+
+// The device's status word and number of SMs, looked up once per device.
+struct DeviceInfo {
+  unsigned* watchdog;
+  int sms;
+};
+cudaError_t device_info(DeviceInfo* out) {
+  static std::atomic<unsigned*> words[64];
+  static std::atomic<int> sms[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  out->watchdog = words[dev].load();
+  out->sms = sms[dev].load();
+  if (out->watchdog != nullptr && out->sms > 0) return cudaSuccess;
+  e = pf::watchdog_word(&out->watchdog);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&out->sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  words[dev].store(out->watchdog);
+  sms[dev].store(out->sms);
+  return cudaSuccess;
+}
+
+pf_status from_attn(cudaError_t e) { return e == cudaErrorNotSupported ? PF_ERR_UNSUPPORTED : from_cuda(e); }
 
 }  // namespace
 
@@ -218,6 +299,36 @@ pf_status pf_qk_norm_rope_bwd(const pf_rope_config* cfg, const float* pos, const
   a.pos = pos;
   return from_cuda(pf::launch_qk_norm_rope_bwd(a, dgain_q, dgain_k, static_cast<float*>(workspace),
                                                static_cast<cudaStream_t>(stream)));
+}
+
+pf_status pf_masked_attn(const pf_masked_attn_config* cfg, const void* q, const void* k, const void* v,
+                         const float* slopes, const int32_t* prefix, const int32_t* doc_q, const int32_t* doc_k,
+                         void* o, float* lse, void* stream) {
+  pf_status st = check_masked(cfg);
+  if (st != PF_OK) return st;
+  const pf_masked_attn_config& c = *cfg;
+  pf::MaskedFwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = make_mask(c, slopes, prefix, doc_q, doc_k, p.m);
+  if (st != PF_OK) return st;
+  if (c.n_q == 0) return PF_OK;
+  if (!q || !o || (c.n_k > 0 && (!k || !v))) return PF_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4)) return PF_ERR_ALIGN;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return PF_ERR_CUDA;
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.watchdog = dev.watchdog;
+  p.batch = c.batch;
+  p.heads_q = c.heads_q;
+  p.heads_kv = c.heads_kv;
+  p.head_dim = c.head_dim;
+  pf::masked_fwd_plan(p, dev.sms);
+  if (!pf::encode_heads_map(&p.tm_q, q, c.batch, c.n_q, c.heads_q, c.head_dim, c.q, p.pack, 128 / p.pack) ||
+      (c.n_k > 0 && (!pf::encode_heads_map(&p.tm_k, k, c.batch, c.n_k, c.heads_kv, c.head_dim, c.k, 1, 128) ||
+                     !pf::encode_heads_map(&p.tm_v, v, c.batch, c.n_k, c.heads_kv, c.head_dim, c.v, 1, 128))))
+    return PF_ERR_CUDA;
+  return from_attn(pf::launch_masked_fwd(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

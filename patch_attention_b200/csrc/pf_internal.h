@@ -142,6 +142,43 @@ int rope_bwd_blocks(const RopeArgs& a);
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, void* dgain_q, void* dgain_k, float* part, cudaStream_t stream);
 
+// 4-D tensor map [batch][rows][heads][d] bf16 with element strides `st` (batch, token, head) and a box
+// of 64 columns x box_heads x box_rows, 128-byte swizzle; the stride of an extent of 1 is not used.
+bool encode_heads_map(CUtensorMap* m, const void* base, int batch, int rows, int heads, int d, const pf_strides& st,
+                      int box_heads, int box_rows);
+
+// Masked attention.  Which keys a query sees and how its scores are changed; scores are kept
+// in units of log2.
+struct MaskParams {
+  const int* prefix;    // [batch] or null
+  const int* doc_q;     // [batch, n_q], with doc_k [batch, n_k], or both null
+  const int* doc_k;
+  const float* slopes;  // [heads_q] or null
+  int causal, n_q, n_k;
+  float scale_log2;     // softmax scale * log2(e)
+  float cap_log2;       // cap * log2(e); 0: no cap
+  float cap_in;         // 2 scale / cap * log2(e)
+};
+struct MaskedFwdParams {
+  CUtensorMap tm_q, tm_k, tm_v;  // 4-D [batch][rows][heads][d]; q's box is pack heads x 128 / pack rows
+  uint16_t* o;                   // [batch, n_q, heads_q, d] bf16
+  float* lse;                    // [batch, heads_q, n_q] or null
+  unsigned* watchdog;
+  MaskParams m;
+  int batch, heads_q, heads_kv, head_dim;
+  int pack;       // query heads of one key head that share a tile (1: one head per tile)
+  int n_groups;   // query-tile groups per head (block)
+  int n_split;    // CTAs (a cluster) that share a query tile's keys
+  int cls_bytes;  // shared bytes for the documents' tile classes
+};
+constexpr int kMaskedDocTiles = 8192;  // key tiles that a call with documents may have
+// Query tiles per CTA, heads per tile and key split of a call.
+void masked_fwd_plan(MaskedFwdParams& p, int n_sms);
+cudaError_t launch_masked_fwd(const MaskedFwdParams& p, cudaStream_t stream);
+
+// Address of the current device's status word.
+cudaError_t watchdog_word(unsigned** word);
+
 // Device word written by kernels whose bounded waits expired (0 = none).
 cudaError_t read_and_clear_watchdog(unsigned* value);
 
