@@ -291,6 +291,24 @@ pf_status pf_masked_attn(const pf_masked_attn_config* cfg, const void* q, const 
                          const int32_t* doc_q, const int32_t* doc_k, void* o, float* lse,
                          void* stream);
 
+/* Workspace bytes of pf_masked_attn_bwd (0 if cfg is invalid or there are no queries). */
+size_t pf_masked_attn_bwd_workspace_bytes(const pf_masked_attn_config* cfg);
+
+/* Gradients of pf_masked_attn (slopes are constants).  q, k, v and the rule as in the forward call, o
+ * and lse as it wrote them.
+ *   dout       : device bf16 [batch, n_q, heads_q, d] contiguous, as dq
+ *   dq, dk, dv : device bf16, contiguous, none overlapping an input; dk and dv [batch, n_k, heads_kv, d]
+ *                are summed over the query heads of each key head.  Equal inputs give equal bits.
+ *   workspace  : 16-byte aligned device scratch, no initialisation needed, one per concurrently
+ *                running call
+ * Queries that see no key have dq = 0 and add nothing, whatever q, dout and o hold there; so do
+ * keys that no query sees.  With documents n_q is at most 2^20 too. */
+pf_status pf_masked_attn_bwd(const pf_masked_attn_config* cfg, const void* dout, const void* q,
+                             const void* k, const void* v, const void* o, const float* lse,
+                             const float* slopes, const int32_t* prefix, const int32_t* doc_q,
+                             const int32_t* doc_k, void* dq, void* dk, void* dv, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* pf_check_device_status for operators that have no context. */
 pf_status pf_device_status(void* stream);
 

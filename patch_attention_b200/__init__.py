@@ -40,7 +40,8 @@ EXPORTED = [
     "pf_check_device_status", "pf_selftest_bounded_wait", "pf_status_string", "pf_version", "pf_switch_init",
     "pf_switch_update", "pf_text_attn_step", "pf_qk_rmsnorm", "pf_get_read_half",
     "pf_layernorm", "pf_layernorm_bwd", "pf_layernorm_bwd_workspace_bytes", "pf_qk_norm_rope",
-    "pf_qk_norm_rope_bwd", "pf_qk_norm_rope_bwd_workspace_bytes", "pf_masked_attn", "pf_device_status",
+    "pf_qk_norm_rope_bwd", "pf_qk_norm_rope_bwd_workspace_bytes", "pf_masked_attn", "pf_masked_attn_bwd",
+    "pf_masked_attn_bwd_workspace_bytes", "pf_device_status",
 ]
 
 PF_BF16 = 0
@@ -139,6 +140,8 @@ def _lib():
             "pf_qk_norm_rope_bwd": (i, [ctypes.POINTER(pf_rope_config), vp] + [vp, stp] * 4 + [vp, vp, vp, stp, vp, stp,
                                         vp, vp, vp, sz, vp]),
             "pf_masked_attn": (i, [ctypes.POINTER(pf_masked_attn_config)] + [vp] * 10),
+            "pf_masked_attn_bwd": (i, [ctypes.POINTER(pf_masked_attn_config)] + [vp] * 14 + [sz, vp]),
+            "pf_masked_attn_bwd_workspace_bytes": (sz, [ctypes.POINTER(pf_masked_attn_config)]),
             "pf_device_status": (i, [vp]),
             "pf_qk_norm_rope_bwd_workspace_bytes": (sz, [ctypes.POINTER(pf_rope_config)]),
         }
@@ -451,6 +454,8 @@ def cfg_combine_relmae(eps_c: torch.Tensor, eps_u: torch.Tensor, w: float, want_
 
 
 from .block import (  # noqa: E402  (needs the names above)
-    RopeAxes, ScoreRule, layernorm, layernorm_backward, masked_attention, pf_device_status, pf_layernorm,
-    pf_layernorm_bwd, pf_layernorm_bwd_workspace_bytes, pf_masked_attn, pf_qk_norm_rope, pf_qk_norm_rope_bwd,
+    RopeAxes, ScoreRule, layernorm, layernorm_backward, masked_attention, masked_attention_backward,
+    pf_device_status, pf_layernorm,
+    pf_layernorm_bwd, pf_layernorm_bwd_workspace_bytes, pf_masked_attn, pf_masked_attn_bwd,
+    pf_masked_attn_bwd_workspace_bytes, pf_qk_norm_rope, pf_qk_norm_rope_bwd,
     pf_qk_norm_rope_bwd_workspace_bytes, qk_norm_rope, qk_norm_rope_backward)

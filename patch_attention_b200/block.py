@@ -399,3 +399,34 @@ def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rule: Op
             lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
         pf_masked_attn(q, k, v, o, lse, rule)
     return (o, lse) if want_lse else o
+
+
+def pf_masked_attn_bwd_workspace_bytes(cfg: pf_masked_attn_config) -> int:
+    return int(_lib().pf_masked_attn_bwd_workspace_bytes(cfg))
+
+
+def pf_masked_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                       lse: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor,
+                       workspace: torch.Tensor, rule: Optional[ScoreRule] = None, stream=None) -> None:
+    rule = rule or _PLAIN
+    dev = _device(q, k, v, dout, o, lse, dq, dk, dv, workspace, *rule.tensors())
+    cfg, ptrs, extra = _masked_args(q, k, v, rule)
+    bf = torch.bfloat16
+    dop, op, dqp = (_whole(t, bf, q.shape, n) for t, n in ((dout, "dout"), (o, "o"), (dq, "dq")))
+    dkp, dvp = (_whole(t, bf, k.shape, n) for t, n in ((dk, "dk"), (dv, "dv")))
+    lp = _whole(lse, torch.float32, (q.shape[0], q.shape[2], q.shape[1]), "lse")
+    wp = _whole(workspace, torch.uint8, workspace.shape, "workspace")
+    with _on(dev, stream):
+        _check(_lib().pf_masked_attn_bwd(cfg, dop, *ptrs, op, lp, *extra, dqp, dkp, dvp, wp, workspace.numel(),
+                                         _raw_stream(dev)), "pf_masked_attn_bwd")
+
+
+def masked_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                              lse: torch.Tensor, rule: Optional[ScoreRule] = None, *, stream=None):
+    """(dq, dk, dv) of ``masked_attention`` from the gradient of its output, its inputs, and the o and lse that it
+    returned; contiguous, dk and dv summed over the query heads that share a key head."""
+    with _on(_device(q), stream):
+        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        ws = torch.empty(4 * q.shape[0] * q.shape[1] * q.shape[2], dtype=torch.uint8, device=q.device)
+        pf_masked_attn_bwd(dout, q, k, v, o, lse, dq, dk, dv, ws, rule)
+    return dq, dk, dv

@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libpatchattn.so")
 OBJDIR = os.path.join(HERE, "_build")
 
 SOURCES = ["attn_fwd.cu", "cfg_combine.cu", "kvbuf_copy.cu", "qk_rmsnorm.cu", "layernorm.cu",
-           "qk_norm_rope.cu", "masked_attn.cu", "pf_api.cpp", "pf_block_api.cpp"]
+           "qk_norm_rope.cu", "masked_attn.cu",
+           "masked_attn_bwd.cu", "pf_api.cpp", "pf_block_api.cpp"]
 HEADERS = ["pf_internal.h", "sm100_ptx.cuh", "block_ops.cuh", "masked_common.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

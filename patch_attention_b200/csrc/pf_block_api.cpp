@@ -126,13 +126,23 @@ pf_status check_strides(const pf_strides& s, int batch, int rows, int heads) {
   return PF_OK;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+float scale_of(const pf_masked_attn_config& c) {
+  return c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / std::sqrt(static_cast<float>(c.head_dim));
+}
+// 2 scale / cap in units of log2: the exponent of the cap's tanh.
+float cap_in_of(const pf_masked_attn_config& c) { return c.softcap > 0.f ? 2.f * scale_of(c) / c.softcap * kLog2e : 0.f; }
+
 pf_status check_masked(const pf_masked_attn_config* c) {
   if (!c) return PF_ERR_INVALID_ARG;
   if (c->batch < 1 || c->heads_q < 1 || c->heads_kv < 1 || c->heads_q % c->heads_kv != 0) return PF_ERR_SHAPE;
   if (c->n_q < 0 || c->n_k < 0 || c->n_q > kMaxTokens || c->n_k > kMaxTokens) return PF_ERR_SHAPE;
   if (c->head_dim != 64 && c->head_dim != 72 && c->head_dim != 128) return PF_ERR_UNSUPPORTED;
   if (!(c->softmax_scale >= 0.f) || std::isinf(c->softmax_scale)) return PF_ERR_INVALID_ARG;
-  if (!(c->softcap >= 0.f) || std::isinf(c->softcap)) return PF_ERR_INVALID_ARG;
+  if (!(c->softcap >= 0.f) || !std::isfinite(c->softcap * kLog2e) || !std::isfinite(scale_of(*c) * kLog2e) ||
+      !std::isfinite(cap_in_of(*c)))
+    return PF_ERR_INVALID_ARG;
   // CTAs (at most 8 per query tile and head, or per key tile) on a 31-bit grid
   const double longest = c->n_q > c->n_k ? c->n_q : c->n_k;
   if (static_cast<double>(c->batch) * c->heads_q * (longest / 128 + 1) * 8 > 2147483647.0) return PF_ERR_SHAPE;
@@ -149,8 +159,6 @@ pf_status make_mask(const pf_masked_attn_config& c, const float* slopes, const i
   const bool docs = doc_q && doc_k;
   if (docs && c.n_k > pf::kMaskedDocTiles * 128) return PF_ERR_SHAPE;
   if (!aligned(slopes, 4) || !aligned(prefix, 4) || !aligned(doc_q, 4) || !aligned(doc_k, 4)) return PF_ERR_ALIGN;
-  const float scale = c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / std::sqrt(static_cast<float>(c.head_dim));
-  const float log2e = 1.4426950408889634f;
   m.prefix = prefix;
   m.doc_q = docs ? doc_q : nullptr;
   m.doc_k = docs ? doc_k : nullptr;
@@ -158,10 +166,9 @@ pf_status make_mask(const pf_masked_attn_config& c, const float* slopes, const i
   m.causal = c.causal != 0;
   m.n_q = c.n_q;
   m.n_k = c.n_k;
-  m.scale_log2 = scale * log2e;
-  m.cap_log2 = c.softcap * log2e;
-  m.cap_in = c.softcap > 0.f ? 2.f * scale / c.softcap * log2e : 0.f;
-  if (!std::isfinite(m.scale_log2) || !std::isfinite(m.cap_log2) || !std::isfinite(m.cap_in)) return PF_ERR_INVALID_ARG;
+  m.scale_log2 = scale_of(c) * kLog2e;
+  m.cap_log2 = c.softcap * kLog2e;
+  m.cap_in = cap_in_of(c);
   return PF_OK;
 }
 
@@ -329,6 +336,58 @@ pf_status pf_masked_attn(const pf_masked_attn_config* cfg, const void* q, const 
                      !pf::encode_heads_map(&p.tm_v, v, c.batch, c.n_k, c.heads_kv, c.head_dim, c.v, 1, 128))))
     return PF_ERR_CUDA;
   return from_attn(pf::launch_masked_fwd(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pf_masked_attn_bwd_workspace_bytes(const pf_masked_attn_config* cfg) {
+  if (check_masked(cfg) != PF_OK) return 0;
+  return static_cast<size_t>(cfg->batch) * cfg->heads_q * cfg->n_q * 4;
+}
+
+pf_status pf_masked_attn_bwd(const pf_masked_attn_config* cfg, const void* dout, const void* q, const void* k,
+                             const void* v, const void* o, const float* lse, const float* slopes,
+                             const int32_t* prefix, const int32_t* doc_q, const int32_t* doc_k, void* dq, void* dk,
+                             void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  pf_status st = check_masked(cfg);
+  if (st != PF_OK) return st;
+  const pf_masked_attn_config& c = *cfg;
+  pf::MaskedBwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = make_mask(c, slopes, prefix, doc_q, doc_k, p.m);
+  if (st != PF_OK) return st;
+  if (p.m.doc_q && c.n_q > pf::kMaskedDocTiles * 128) return PF_ERR_SHAPE;
+  if (c.n_q > 0 && (!dout || !q || !o || !lse || !dq || !workspace)) return PF_ERR_INVALID_ARG;
+  if (c.n_k > 0 && (!k || !v || !dk || !dv)) return PF_ERR_INVALID_ARG;
+  const void* all[] = {dout, q, k, v, o, dq, dk, dv, workspace};
+  for (const void* x : all)
+    if (!aligned(x, 16)) return PF_ERR_ALIGN;
+  if (!aligned(lse, 4)) return PF_ERR_ALIGN;
+  if (workspace_bytes < pf_masked_attn_bwd_workspace_bytes(cfg)) return PF_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return PF_ERR_CUDA;
+  p.o = static_cast<const uint16_t*>(o);
+  p.dout = static_cast<const uint16_t*>(dout);
+  p.lse = lse;
+  p.delta = static_cast<float*>(workspace);
+  p.dq = static_cast<uint16_t*>(dq);
+  p.dk = static_cast<uint16_t*>(dk);
+  p.dv = static_cast<uint16_t*>(dv);
+  p.watchdog = dev.watchdog;
+  p.batch = c.batch;
+  p.heads_q = c.heads_q;
+  p.heads_kv = c.heads_kv;
+  p.head_dim = c.head_dim;
+  p.scale = scale_of(c);
+  const int64_t row = static_cast<int64_t>(c.heads_q) * c.head_dim;
+  const pf_strides whole = {row * c.n_q, row, c.head_dim};
+  CUtensorMap maps[4];
+  std::memset(maps, 0, sizeof(maps));
+  if (c.n_q > 0 && (!pf::encode_heads_map(&maps[0], q, c.batch, c.n_q, c.heads_q, c.head_dim, c.q, 1, 128) ||
+                    !pf::encode_heads_map(&maps[3], dout, c.batch, c.n_q, c.heads_q, c.head_dim, whole, 1, 128)))
+    return PF_ERR_CUDA;
+  if (c.n_k > 0 && (!pf::encode_heads_map(&maps[1], k, c.batch, c.n_k, c.heads_kv, c.head_dim, c.k, 1, 128) ||
+                    !pf::encode_heads_map(&maps[2], v, c.batch, c.n_k, c.heads_kv, c.head_dim, c.v, 1, 128)))
+    return PF_ERR_CUDA;
+  return from_attn(pf::launch_masked_bwd(p, maps, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -176,6 +176,23 @@ constexpr int kMaskedDocTiles = 8192;  // key tiles that a call with documents m
 void masked_fwd_plan(MaskedFwdParams& p, int n_sms);
 cudaError_t launch_masked_fwd(const MaskedFwdParams& p, cudaStream_t stream);
 
+struct MaskedBwdParams {
+  CUtensorMap tm_x1, tm_x2, tm_y1, tm_y2;  // staying and streaming tiles (set by the launch)
+  const uint16_t* o;                       // o, dout: [batch, n_q, heads_q, d]
+  const uint16_t* dout;
+  const float* lse;                        // [batch, heads_q, n_q], as delta
+  float* delta;                            // workspace
+  uint16_t* dq;                            // contiguous, as q, k, v
+  uint16_t* dk;
+  uint16_t* dv;
+  unsigned* watchdog;
+  MaskParams m;
+  int batch, heads_q, heads_kv, head_dim;
+  float scale;
+};
+// maps: q, k, v, dout with boxes of one head x 128 rows.
+cudaError_t launch_masked_bwd(MaskedBwdParams& p, const CUtensorMap (&maps)[4], cudaStream_t stream);
+
 // Address of the current device's status word.
 cudaError_t watchdog_word(unsigned** word);
 

@@ -133,6 +133,77 @@ def test_rope_backward():
     assert call(_rope_cfg(eps=0.0)) == pa.PF_ERR_INVALID_ARG  # gain gradients without a norm
 
 
+def _attn_cfg(**kw):
+    a = dict(batch=2, heads_q=4, heads_kv=2, head_dim=64, n_q=10, n_k=20, softmax_scale=0.0, softcap=0.0, causal=1,
+             q=(2560, 256, 64), k=(2560, 128, 64), v=(2560, 128, 64))
+    a.update(kw)
+    return pa.pf_masked_attn_config(a["batch"], a["heads_q"], a["heads_kv"], a["head_dim"], a["n_q"], a["n_k"],
+                                    a["softmax_scale"], a["softcap"], a["causal"], pa.pf_strides(*a["q"]),
+                                    pa.pf_strides(*a["k"]), pa.pf_strides(*a["v"]))
+
+
+def _attn(cfg, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, slopes=None, prefix=None, doc_q=None, doc_k=None, o=FAKE, lse=None)
+    a.update(kw)
+    return pa._lib().pf_masked_attn(cfg, *a.values(), None)
+
+
+def _attn_bwd(cfg, **kw):
+    a = dict(dout=FAKE, q=FAKE, k=FAKE, v=FAKE, o=FAKE, lse=FAKE, slopes=None, prefix=None, doc_q=None, doc_k=None,
+             dq=FAKE, dk=FAKE, dv=FAKE, work=FAKE, bytes=1 << 20)
+    a.update(kw)
+    return pa._lib().pf_masked_attn_bwd(cfg, *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=0), pa.PF_ERR_SHAPE), (dict(heads_q=5), pa.PF_ERR_SHAPE), (dict(heads_kv=0), pa.PF_ERR_SHAPE),
+    (dict(heads_q=0), pa.PF_ERR_SHAPE), (dict(n_q=-1), pa.PF_ERR_SHAPE), (dict(n_k=-1), pa.PF_ERR_SHAPE),
+    (dict(n_k=(1 << 30) + 1), pa.PF_ERR_SHAPE), (dict(batch=1 << 16, heads_q=1 << 10, n_q=1 << 20), pa.PF_ERR_SHAPE),
+    (dict(head_dim=96), pa.PF_ERR_UNSUPPORTED), (dict(softmax_scale=-1.0), pa.PF_ERR_INVALID_ARG),
+    (dict(softmax_scale=float("nan")), pa.PF_ERR_INVALID_ARG), (dict(softcap=-1.0), pa.PF_ERR_INVALID_ARG),
+    (dict(softcap=float("inf")), pa.PF_ERR_INVALID_ARG), (dict(softcap=1e-38, softmax_scale=1e30), pa.PF_ERR_INVALID_ARG),
+    (dict(q=(2560, 260, 64)), pa.PF_ERR_ALIGN), (dict(k=(2560, 0, 64)), pa.PF_ERR_INVALID_ARG),
+    (dict(v=(2560, -128, 64)), pa.PF_ERR_INVALID_ARG), (dict(v=(1 << 39, 128, 64)), pa.PF_ERR_INVALID_ARG),
+])
+def test_masked_attention_config(kw, status):
+    cfg = _attn_cfg(**kw)
+    assert _attn(cfg) == status and _attn_bwd(cfg) == status
+    assert pa.pf_masked_attn_bwd_workspace_bytes(cfg) == 0
+
+
+def test_masked_attention_operands():
+    cfg = _attn_cfg()
+    for name in ("q", "k", "v", "o"):
+        assert _attn(cfg, **{name: None}) == pa.PF_ERR_INVALID_ARG
+        assert _attn(cfg, **{name: FAKE + 8}) == pa.PF_ERR_ALIGN
+    for name in ("dout", "q", "k", "v", "o", "dq", "dk", "dv", "work"):
+        assert _attn_bwd(cfg, **{name: None}) == pa.PF_ERR_INVALID_ARG
+        assert _attn_bwd(cfg, **{name: FAKE + 8}) == pa.PF_ERR_ALIGN
+    assert _attn_bwd(cfg, lse=None) == pa.PF_ERR_INVALID_ARG and _attn_bwd(cfg, lse=FAKE + 2) == pa.PF_ERR_ALIGN
+    assert _attn(cfg, lse=FAKE + 2) == pa.PF_ERR_ALIGN
+    need = pa.pf_masked_attn_bwd_workspace_bytes(cfg)
+    assert need == 2 * 4 * 10 * 4 and _attn_bwd(cfg, bytes=need - 1) == pa.PF_ERR_INVALID_ARG
+    # masks: a prefix without a causal mask, one side's documents, too many keys for documents
+    assert _attn(_attn_cfg(causal=0), prefix=FAKE) == pa.PF_ERR_INVALID_ARG
+    assert _attn(cfg, doc_q=FAKE) == pa.PF_ERR_INVALID_ARG and _attn(cfg, doc_k=FAKE) == pa.PF_ERR_INVALID_ARG
+    assert _attn(cfg, doc_q=FAKE + 2, doc_k=FAKE) == pa.PF_ERR_ALIGN
+    assert _attn(_attn_cfg(n_k=(1 << 20) + 1), doc_q=FAKE, doc_k=FAKE) == pa.PF_ERR_SHAPE
+    assert _attn_bwd(_attn_cfg(n_q=(1 << 20) + 1), doc_q=FAKE, doc_k=FAKE) == pa.PF_ERR_SHAPE
+    assert _attn(None) == pa.PF_ERR_INVALID_ARG and _attn_bwd(None) == pa.PF_ERR_INVALID_ARG
+    assert _attn(_attn_cfg(n_q=0), q=None, o=None) == pa.PF_OK
+
+
+def test_score_rule():
+    t = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        pa.ScoreRule(prefix=t)
+    with pytest.raises(ValueError):
+        pa.ScoreRule(doc_q=t)
+    q = torch.zeros(1, 2, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        pa.masked_attention(q, q, q)  # not on a GPU
+
+
 def test_python_refuses_cpu_tensors_and_bad_layouts():
     x = torch.zeros(2, 3, 64)
     with pytest.raises(ValueError):
