@@ -7,12 +7,20 @@
 //   dw_g = sum over the group's rows of dy x^,  db_g = sum of dy
 //
 // Both directions are HBM bound: forward reads x and writes y, backward reads x and dy and
-// writes dx.  A row is read once and stays in registers, so the variance is taken around the
-// mean (two passes over registers, none over memory).  Rows up to 1536 elements belong to one
-// warp (no block barrier; many rows in flight per SM); wider ones to a block of 128 or 512
-// threads.  The backward pass keeps the weight-gradient sums of its columns in registers over
-// a contiguous run of rows and writes one fp32 partial row per block; a second kernel adds
-// the partials in a fixed order, so equal inputs give equal bits.
+// writes dx.  A row of up to 2048 elements belongs to one warp, so that it needs no barrier and
+// its fixed cost (two shuffle trees) is spread over up to 64 elements per lane; wider rows belong
+// to a block of up to 16 warps.  The forward pass reads a row into registers once.  The backward
+// pass walks rows: it keeps the weight-gradient sums of a lane's columns in registers, and the
+// next row of x and dy is copied into shared memory (each lane its own elements, so no barrier)
+// while the current one is worked on.  Arithmetic is on pairs (two fp32 lanes per instruction):
+// element by element, instruction issue was the bound (25 instructions per element forward).
+// The variance is taken around means: a warp's around its own; in wider rows the warps' (mean, sum
+// of squares) are then combined.
+//
+// The backward pass writes one fp32 partial row of the weight gradients per block; a second
+// kernel adds the partials in a fixed order, so equal inputs give equal bits.
+
+#include <mutex>
 
 #include "block_ops.cuh"
 
@@ -32,218 +40,381 @@ struct LnParams {
   float* part;         // backward: [group][part][2][channels] partial sums, or null
   long long rows, rows_per_group, weight_stride, bias_stride;
   int channels, parts;
+  int warps;           // warps per row
+  int stages;          // backward: rows of shared memory per warp, 2 (or 1 where 2 do not fit)
   int wide;            // the parameters are fp32 (else the type of x)
   float w0, eps;
 };
 
-// Sum of two values over a team: a warp, or the whole block (then `scratch` holds 2 x 16
-// values per parity so that consecutive calls need one barrier each).
-template <int TEAM>
-__device__ __forceinline__ void team_sum2(float& a, float& b, float (*scratch)[2][16], int& parity) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if constexpr (TEAM > 32) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) {
-      scratch[parity][0][warp] = a;
-      scratch[parity][1][warp] = b;
-    }
-    __syncthreads();
-    a = lane < TEAM / 32 ? scratch[parity][0][lane] : 0.f;
-    b = lane < TEAM / 32 ? scratch[parity][1][lane] : 0.f;
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <typename T>
+__device__ __forceinline__ float2 pair_of(const T* v) {
+  return make_float2(to_f<T>(v[0]), to_f<T>(v[1]));
+}
+template <>
+__device__ __forceinline__ float2 pair_of<__nv_bfloat16>(const __nv_bfloat16* v) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(v);
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 pair_of<__half>(const __half* v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(v));
+}
+template <typename T>
+__device__ __forceinline__ void put_pair(T* to, float2 f) {
+  to[0] = from_f<T>(f.x);
+  to[1] = from_f<T>(f.y);
+}
+template <>
+__device__ __forceinline__ void put_pair<__nv_bfloat16>(__nv_bfloat16* to, float2 f) {
+  *reinterpret_cast<__nv_bfloat162*>(to) = __floats2bfloat162_rn(f.x, f.y);
+}
+template <>
+__device__ __forceinline__ void put_pair<__half>(__half* to, float2 f) {
+  *reinterpret_cast<__half2*>(to) = __floats2half2_rn(f.x, f.y);
+}
+
+// A lane's columns: unit i (VEC consecutive elements) of EPT / VEC starts at column(i).
+template <int VEC>
+struct Place {
+  int first;
+  __device__ __forceinline__ int column(int i) const { return first + i * 32 * VEC; }
+};
+
+// One pair of elements at a time from registers, shared or global memory: U is a unit.
+// Pair k is elements 2k, 2k + 1 of the lane: inside unit 2k / VEC, or (VEC = 1) units 2k, 2k + 1.
+template <typename T, int VEC>
+using Unit = Vec<T, VEC>;
+
+// The lane's parameters of unit group `k` (one unit, or two for VEC = 1) as pairs.
+template <typename T, int VEC, int N>
+__device__ __forceinline__ void unit_params(float2 (&f)[N], const void* base, long long row, float plus, float none,
+                                            int k, const LnParams& p, const Place<VEC>& at) {
+  if constexpr (VEC == 1) {
+    float v[2] = {none, none};
 #pragma unroll
-    for (int off = TEAM / 64; off > 0; off >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, off);
-      b += __shfl_xor_sync(0xffffffffu, b, off);
+    for (int u = 0; u < 2; ++u) {
+      const int c = at.column(2 * k + u);
+      if (base != nullptr && c < p.channels) {
+        float x[1];
+        load_param<T, 1>(base, row + c, p.wide, x);
+        v[u] = x[0] + plus;
+      }
     }
-    a = __shfl_sync(0xffffffffu, a, 0);
-    b = __shfl_sync(0xffffffffu, b, 0);
-    parity ^= 1;
+    f[0] = make_float2(v[0], v[1]);
+  } else {
+    if (base != nullptr) {
+      if (p.wide) {
+        float v[VEC];
+        load_param<T, VEC>(base, row + at.column(k), true, v);
+#pragma unroll
+        for (int u = 0; u < VEC / 2; ++u) f[u] = add2(make_float2(v[2 * u], v[2 * u + 1]), both(plus));
+      } else {
+        const Unit<T, VEC> v = load_vec<T, VEC>(static_cast<const T*>(base) + row + at.column(k));
+#pragma unroll
+        for (int u = 0; u < VEC / 2; ++u) f[u] = add2(pair_of<T>(v.v + 2 * u), both(plus));
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < VEC / 2; ++u) f[u] = both(none);
+    }
   }
 }
 
-template <typename T, int VEC, int TEAM, int EPT>
-__global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) ln_fwd_kernel(const __grid_constant__ LnParams p) {
-  constexpr int NV = EPT / VEC;
-  __shared__ float scratch[2][2][16];
+// How the units of a lane are walked: K groups, each of P pairs.
+template <int VEC, int EPT>
+struct Walk {
+  static constexpr int P = VEC == 1 ? 1 : VEC / 2;
+  static constexpr int K = EPT / 2 / P;
+};
+
+// Two values summed over the row's warps.  Consecutive calls alternate between two buffers, so
+// one barrier each is enough.
+struct Exchange {
+  float2 (*slots)[16];  // [parity][warp]
   int parity = 0;
-  const int t = TEAM == 32 ? threadIdx.x & 31 : threadIdx.x;
-  const long long row = TEAM == 32 ? static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)
-                                   : static_cast<long long>(blockIdx.x);
-  if (row >= p.rows) return;  // whole teams leave
-  const T* x = static_cast<const T*>(p.x) + row * p.channels;
-  Vec<T, VEC> raw[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * TEAM + t) * VEC;
-    if (c < p.channels) raw[i] = load_vec<T, VEC>(x + c);
+  __device__ __forceinline__ const float2* publish(float2 v, int warp, int lane) {
+    float2* mine = slots[parity];
+    parity ^= 1;
+    if (lane == 0) mine[warp] = v;
+    __syncthreads();
+    return mine;
   }
-  float s = 0.f, unused = 0.f;
+};
+
+// Rows of one warp: `blockDim.x / 32` rows per block.  Wider rows (WIDE): one row per block.
+template <typename T, int VEC, int EPT, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 512 : 128) ln_fwd_kernel(const __grid_constant__ LnParams p) {
+  using Wk = Walk<VEC, EPT>;
+  __shared__ float2 slots[2][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row = WIDE ? blockIdx.x : static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
+  if (row >= p.rows) return;
+  const int n = p.channels;
+  const int first = WIDE ? warp * 32 * EPT : 0;  // this warp's columns
+  const float mine = static_cast<float>(min(max(n - first, 0), 32 * EPT));
+  const Place<VEC> at = {first + lane * VEC};
+  const T* x = static_cast<const T*>(p.x) + row * n;
+  Unit<T, VEC> raw[EPT / VEC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if ((i * TEAM + t) * VEC < p.channels) {
+  for (int i = 0; i < EPT / VEC; ++i)
+    if (at.column(i) < n) raw[i] = load_vec<T, VEC>(x + at.column(i));
+  float2 f[EPT / 2];
+  float2 s2 = both(0.f);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) s += to_f<T>(raw[i].v[k]);
-    }
-  team_sum2<TEAM>(s, unused, scratch, parity);
-  const float inv_n = 1.f / static_cast<float>(p.channels);
-  const float mean = s * inv_n;
-  float ss = 0.f;
+  for (int k = 0; k < Wk::K; ++k) {
+    if constexpr (VEC == 1) {
+      f[k].x = at.column(2 * k) < n ? to_f<T>(raw[2 * k].v[0]) : 0.f;
+      f[k].y = at.column(2 * k + 1) < n ? to_f<T>(raw[2 * k + 1].v[0]) : 0.f;
+      s2 = add2(s2, f[k]);
+    } else if (at.column(k) < n) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if ((i * TEAM + t) * VEC < p.channels) {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const float d = to_f<T>(raw[i].v[k]) - mean;
-        ss = fmaf(d, d, ss);
+      for (int u = 0; u < Wk::P; ++u) {
+        f[k * Wk::P + u] = pair_of<T>(raw[k].v + 2 * u);
+        s2 = add2(s2, f[k * Wk::P + u]);
       }
     }
-  team_sum2<TEAM>(ss, unused, scratch, parity);
-  const float rstd = rsqrtf(fmaf(ss, inv_n, p.eps));
-  if (t == 0) {
+  }
+  float mean = warp_sum(s2.x + s2.y) * (mine > 0.f ? 1.f / mine : 0.f);
+  float2 q2 = both(0.f);
+#pragma unroll
+  for (int k = 0; k < Wk::K; ++k) {
+    if constexpr (VEC == 1) {
+      float2 d = add2(f[k], both(-mean));
+      if (at.column(2 * k) >= n) d.x = 0.f;
+      if (at.column(2 * k + 1) >= n) d.y = 0.f;
+      q2 = fma2(d, d, q2);
+    } else if (at.column(k) < n) {
+#pragma unroll
+      for (int u = 0; u < Wk::P; ++u) {
+        const float2 d = add2(f[k * Wk::P + u], both(-mean));
+        q2 = fma2(d, d, q2);
+      }
+    }
+  }
+  float sq = warp_sum(q2.x + q2.y);
+  const float inv_n = 1.f / static_cast<float>(n);
+  if constexpr (WIDE) {
+    Exchange ex{slots};
+    const float2* all = ex.publish(make_float2(mean, sq), warp, lane);
+    float m = 0.f, c = 0.f;
+    for (int k = 0; k < p.warps; ++k) m = fmaf(static_cast<float>(min(n - k * 32 * EPT, 32 * EPT)), all[k].x, m);
+    m *= inv_n;
+    for (int k = 0; k < p.warps; ++k) {
+      const float d = all[k].x - m;
+      c += fmaf(static_cast<float>(min(n - k * 32 * EPT, 32 * EPT)) * d, d, all[k].y);
+    }
+    mean = m;
+    sq = c;
+  }
+  const float rstd = rsqrtf(fmaf(sq, inv_n, p.eps));
+  if (lane == 0 && (!WIDE || warp == 0)) {
     if (p.mean != nullptr) p.mean[row] = mean;
     if (p.rstd != nullptr) p.rstd[row] = rstd;
   }
-  const long long g = row / p.rows_per_group;
-  T* y = static_cast<T*>(p.y) + row * p.channels;
+  // row and rows_per_group fit 31 bits
+  const long long g = static_cast<unsigned>(row) / static_cast<unsigned>(p.rows_per_group);
+  T* y = static_cast<T*>(p.y) + row * n;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * TEAM + t) * VEC;
-    if (c < p.channels) {
-      float w[VEC], b[VEC];
+  for (int k = 0; k < Wk::K; ++k) {
+    if (at.column(VEC == 1 ? 2 * k : k) >= n) continue;
+    float2 w[Wk::P], b[Wk::P];
+    unit_params<T, VEC>(w, p.weight, g * p.weight_stride, p.w0, 1.f, k, p, at);
+    unit_params<T, VEC>(b, p.bias, g * p.bias_stride, 0.f, 0.f, k, p, at);
+    Unit<T, VEC> o;
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        w[k] = 1.f;
-        b[k] = 0.f;
+    for (int u = 0; u < Wk::P; ++u) {
+      const float2 v = fma2(mul2(add2(f[k * Wk::P + u], both(-mean)), both(rstd)), w[u], b[u]);
+      if constexpr (VEC == 1) {
+        y[at.column(2 * k)] = from_f<T>(v.x);
+        if (at.column(2 * k + 1) < n) y[at.column(2 * k + 1)] = from_f<T>(v.y);
+      } else {
+        put_pair<T>(o.v + 2 * u, v);
       }
-      if (p.weight != nullptr) {
-        load_param<T, VEC>(p.weight, g * p.weight_stride + c, p.wide, w);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) w[k] += p.w0;
-      }
-      if (p.bias != nullptr) load_param<T, VEC>(p.bias, g * p.bias_stride + c, p.wide, b);
-      Vec<T, VEC> o;
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) o.v[k] = from_f<T>(fmaf((to_f<T>(raw[i].v[k]) - mean) * rstd, w[k], b[k]));
-      store_vec<T, VEC>(y + c, o);
     }
+    if constexpr (VEC > 1) store_vec<T, VEC>(y + at.column(k), o);
   }
 }
 
-template <typename T, int VEC, int TEAM, int EPT>
-__global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) ln_bwd_kernel(const __grid_constant__ LnParams p) {
-  constexpr int NV = EPT / VEC;
-  constexpr int TEAMS = TEAM == 32 ? 4 : 1;
-  __shared__ float scratch[2][2][16];
-  __shared__ float comb[TEAM == 32 ? 2 * 32 * EPT : 1];
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+}
+
+constexpr int kBwdTeams = 4;  // rows in flight per block where a warp takes a row
+
+// Shared bytes: `stages` rows of (x, dy) units per warp, reused for the sums of a block's teams.
+// Single 16-bit elements are not staged: a copy into shared memory is at least 4 bytes.
+constexpr size_t kBwdSmem = 200 * 1024;
+template <typename T, int VEC, int EPT, bool WIDE>
+size_t bwd_smem(int warps, int channels, int stages) {
+  const size_t row = sizeof(T) * VEC < 4 ? 0 : 2 * EPT * 32 * sizeof(T);
+  const size_t ring = (WIDE ? warps : kBwdTeams) * stages * row;
+  const size_t sums = WIDE ? 0 : 2 * static_cast<size_t>(channels) * sizeof(float);
+  return ring > sums ? ring : sums;
+}
+
+template <typename T, int VEC, int EPT, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_kernel(const __grid_constant__ LnParams p) {
+  using Wk = Walk<VEC, EPT>;
+  // else elements are read from global memory, and again in the second pass over the row
+  constexpr bool kRing = sizeof(T) * VEC >= 4;
+  constexpr int kUnits = EPT / VEC;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ float2 slots[2][16];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int parity = 0;
-  const int t = TEAM == 32 ? threadIdx.x & 31 : threadIdx.x;
-  const int team = TEAM == 32 ? threadIdx.x >> 5 : 0;
+  Exchange ex{slots};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = p.channels;
+  const Place<VEC> at = {(WIDE ? warp * 32 * EPT : 0) + lane * VEC};
   const long long g = blockIdx.x / p.parts;
   const int part = static_cast<int>(blockIdx.x % p.parts);
   const long long lo = g * p.rows_per_group + p.rows_per_group * part / p.parts;
   const long long hi = g * p.rows_per_group + p.rows_per_group * (part + 1) / p.parts;
-  const float inv_n = 1.f / static_cast<float>(p.channels);
-  float aw[EPT], ab[EPT];
+  constexpr int kStep = WIDE ? 1 : kBwdTeams;
+  const float inv_n = 1.f / static_cast<float>(n);
+  const T* x = static_cast<const T*>(p.x);
+  const T* dy = static_cast<const T*>(p.dy);
+  // this lane's slots: [stage][x, dy][unit], a unit's lanes side by side
+  Unit<T, VEC>* ring = reinterpret_cast<Unit<T, VEC>*>(dyn) + warp * p.stages * 2 * kUnits * 32 + lane;
+  auto slot = [&](int stage, int which, int i) { return ring + ((stage * 2 + which) * kUnits + i) * 32; };
+  auto fetch = [&](long long row, int stage) {
+    if constexpr (kRing) {
 #pragma unroll
-  for (int k = 0; k < EPT; ++k) aw[k] = ab[k] = 0.f;
-  for (long long row = lo + team; row < hi; row += TEAMS) {
-    const T* x = static_cast<const T*>(p.x) + row * p.channels;
-    const T* dy = static_cast<const T*>(p.dy) + row * p.channels;
-    Vec<T, VEC> rx[NV], rd[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TEAM + t) * VEC;
-      if (c < p.channels) {
-        rx[i] = load_vec<T, VEC>(x + c);
-        rd[i] = load_vec<T, VEC>(dy + c);
-      }
+      for (int i = 0; i < kUnits; ++i)
+        if (at.column(i) < n) {
+          copy_async<sizeof(T) * VEC>(slot(stage, 0, i), x + row * n + at.column(i));
+          copy_async<sizeof(T) * VEC>(slot(stage, 1, i), dy + row * n + at.column(i));
+        }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float sa = 0.f, sx = 0.f;
+  };
+  float2 aw[EPT / 2], ab[EPT / 2];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TEAM + t) * VEC;
-      if (c < p.channels) {
-        float w[VEC];
+  for (int k = 0; k < EPT / 2; ++k) aw[k] = ab[k] = both(0.f);
+  long long row = lo + (WIDE ? 0 : warp);
+  if (row < hi) {
+    fetch(row, 0);
+    float mean = p.mean[row], rstd = p.rstd[row];
+    const int flip = p.stages - 1;
+    for (int stage = 0;; stage ^= flip) {
+      const bool more = row + kStep < hi;
+      float next_mean = 0.f, next_rstd = 0.f;
+      if (more) {
+        if (flip) fetch(row + kStep, stage ^ 1);
+        next_mean = p.mean[row + kStep];
+        next_rstd = p.rstd[row + kStep];
+      }
+      if constexpr (kRing) {
+        // this lane's own copies: nothing to synchronise
+        if (more && flip)
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      // pairs of the row's x (which = 0) or dy (1) in unit group k, 0 past the end
+      auto get = [&](int which, int k, float2(&f)[Wk::P]) {
+        if constexpr (VEC == 1) {
+          const T* src = which ? dy : x;
+          const int c0 = at.column(2 * k), c1 = at.column(2 * k + 1);
+          f[0].x = c0 < n ? to_f<T>(kRing ? slot(stage, which, 2 * k)->v[0] : src[row * n + c0]) : 0.f;
+          f[0].y = c1 < n ? to_f<T>(kRing ? slot(stage, which, 2 * k + 1)->v[0] : src[row * n + c1]) : 0.f;
+        } else {
+          const Unit<T, VEC> v = *slot(stage, which, k);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) w[k] = 1.f;
-        if (p.weight != nullptr) {
-          load_param<T, VEC>(p.weight, g * p.weight_stride + c, p.wide, w);
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) w[k] += p.w0;
+          for (int u = 0; u < Wk::P; ++u) f[u] = pair_of<T>(v.v + 2 * u);
         }
+      };
+      const float2 shift = both(-mean * rstd);
+      float2 s2 = both(0.f), q2 = both(0.f);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const float d = to_f<T>(rd[i].v[k]);
-          const float xh = (to_f<T>(rx[i].v[k]) - mean) * rstd;
-          aw[i * VEC + k] = fmaf(d, xh, aw[i * VEC + k]);
-          ab[i * VEC + k] += d;
-          const float a = d * w[k];
-          sa += a;
-          sx = fmaf(a, xh, sx);
+      for (int k = 0; k < Wk::K; ++k) {
+        if (at.column(VEC == 1 ? 2 * k : k) >= n) continue;
+        float2 xv[Wk::P], dv[Wk::P], w[Wk::P];
+        get(0, k, xv);
+        get(1, k, dv);
+        unit_params<T, VEC>(w, p.weight, g * p.weight_stride, p.w0, 1.f, k, p, at);
+#pragma unroll
+        for (int u = 0; u < Wk::P; ++u) {
+          const int e = k * Wk::P + u;
+          const float2 xh = fma2(xv[u], both(rstd), shift);
+          aw[e] = fma2(dv[u], xh, aw[e]);
+          ab[e] = add2(ab[e], dv[u]);
+          const float2 a = mul2(dv[u], w[u]);
+          s2 = add2(s2, a);
+          q2 = fma2(a, xh, q2);
         }
       }
-    }
-    team_sum2<TEAM>(sa, sx, scratch, parity);
-    sa *= inv_n;
-    sx *= inv_n;
-    T* dx = static_cast<T*>(p.y) + row * p.channels;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TEAM + t) * VEC;
-      if (c < p.channels) {
-        float w[VEC];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) w[k] = 1.f;
-        if (p.weight != nullptr) {
-          load_param<T, VEC>(p.weight, g * p.weight_stride + c, p.wide, w);
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) w[k] += p.w0;
+      float sa = warp_sum(s2.x + s2.y), sx = warp_sum(q2.x + q2.y);
+      if constexpr (WIDE) {
+        const float2* all = ex.publish(make_float2(sa, sx), warp, lane);
+        sa = sx = 0.f;
+        for (int k = 0; k < p.warps; ++k) {
+          sa += all[k].x;
+          sx += all[k].y;
         }
-        Vec<T, VEC> o;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const float xh = (to_f<T>(rx[i].v[k]) - mean) * rstd;
-          o.v[k] = from_f<T>(rstd * (to_f<T>(rd[i].v[k]) * w[k] - sa - xh * sx));
-        }
-        store_vec<T, VEC>(dx + c, o);
       }
+      const float2 c0 = both(-rstd * sa * inv_n), c1 = both(-rstd * sx * inv_n);
+      T* out = static_cast<T*>(p.y) + row * n;
+#pragma unroll
+      for (int k = 0; k < Wk::K; ++k) {
+        if (at.column(VEC == 1 ? 2 * k : k) >= n) continue;
+        float2 xv[Wk::P], dv[Wk::P], w[Wk::P];
+        get(0, k, xv);
+        get(1, k, dv);
+        unit_params<T, VEC>(w, p.weight, g * p.weight_stride, p.w0, 1.f, k, p, at);
+        Unit<T, VEC> o;
+#pragma unroll
+        for (int u = 0; u < Wk::P; ++u) {
+          const float2 xh = fma2(xv[u], both(rstd), shift);
+          const float2 v = fma2(xh, c1, fma2(mul2(dv[u], w[u]), both(rstd), c0));
+          if constexpr (VEC == 1) {
+            out[at.column(2 * k)] = from_f<T>(v.x);
+            if (at.column(2 * k + 1) < n) out[at.column(2 * k + 1)] = from_f<T>(v.y);
+          } else {
+            put_pair<T>(o.v + 2 * u, v);
+          }
+        }
+        if constexpr (VEC > 1) store_vec<T, VEC>(out + at.column(k), o);
+      }
+      if (!more) break;
+      row += kStep;
+      mean = next_mean;
+      rstd = next_rstd;
+      if (!flip) fetch(row, 0);
     }
   }
   if (p.part == nullptr) return;
   // the block's partial: teams add in order, so the result does not depend on timing
-  float* out = p.part + (g * p.parts + part) * 2 * p.channels;
-  if constexpr (TEAM == 32) {
-    for (int w = 0; w < TEAMS; ++w) {
-      if (team == w) {
+  float* out = p.part + (g * p.parts + part) * 2 * n;
+  float* comb = reinterpret_cast<float*>(dyn);
+  __syncthreads();
+  for (int t = 0; t < kStep; ++t) {
+    if (WIDE || warp == t) {
 #pragma unroll
-        for (int k = 0; k < EPT; ++k) {
-          float* a = comb + k * 32 + t;
-          float* b = a + 32 * EPT;
-          *a = w == 0 ? aw[k] : *a + aw[k];
-          *b = w == 0 ? ab[k] : *b + ab[k];
+      for (int e = 0; e < EPT; ++e) {
+        const int c = at.column(e / VEC) + e % VEC;
+        if (c < n) {
+          float u = e & 1 ? aw[e / 2].y : aw[e / 2].x, v = e & 1 ? ab[e / 2].y : ab[e / 2].x;
+          if (t > 0) {
+            u += comb[c];
+            v += comb[n + c];
+          }
+          float* to = t + 1 == kStep ? out : comb;
+          to[c] = u;
+          to[n + c] = v;
         }
       }
-      __syncthreads();
     }
-    for (int e = threadIdx.x; e < 2 * p.channels; e += 128) {
-      const int which = e >= p.channels, c = e - which * p.channels;
-      const int vec = c / VEC, k = c % VEC;  // column c: lane vec % 32, slot (vec / 32) VEC + k
-      out[e] = comb[which * 32 * EPT + ((vec / 32) * VEC + k) * 32 + vec % 32];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const int c = (i * TEAM + t) * VEC + k;
-        if (c < p.channels) {
-          out[c] = aw[i * VEC + k];
-          out[p.channels + c] = ab[i * VEC + k];
-        }
-      }
+    if (!WIDE) __syncthreads();
   }
 }
 
@@ -281,37 +452,73 @@ __global__ void __launch_bounds__(32 * kRedLanes) reduce_parts_kernel(const floa
     static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(s);
 }
 
-template <typename T, int VEC, int TEAM, int EPT>
-cudaError_t launch_team(const LnParams& p, long long groups, bool bwd, cudaStream_t stream) {
-  if (bwd) {
-    ln_bwd_kernel<T, VEC, TEAM, EPT>
-        <<<static_cast<unsigned>(groups * p.parts), TEAM == 32 ? 128 : TEAM, 0, stream>>>(p);
-  } else if (TEAM == 32) {
-    // one warp per block while that still leaves SMs without work, else four
-    const int warps = p.rows <= 148 * 8 ? 1 : 4;
-    ln_fwd_kernel<T, VEC, TEAM, EPT>
-        <<<static_cast<unsigned>((p.rows + warps - 1) / warps), 32 * warps, 0, stream>>>(p);
-  } else {
-    ln_fwd_kernel<T, VEC, TEAM, EPT><<<static_cast<unsigned>(p.rows), TEAM, 0, stream>>>(p);
+constexpr int kSms = 148;
+constexpr int kMostParts = kSms * 8;
+
+// Resident blocks per SM of a backward kernel with rows of `warps` warps, looked up once.
+template <typename T, int VEC, int EPT, bool WIDE>
+cudaError_t bwd_blocks(size_t smem, int warps, int* blocks) {
+  auto kernel = ln_bwd_kernel<T, VEC, EPT, WIDE>;
+  static std::mutex mu;
+  static int known[64][17] = {};  // [device ordinal][warps]
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  int& k = known[dev][warps];
+  if (k == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k, kernel, 32 * (WIDE ? warps : kBwdTeams), smem);
+    if (e != cudaSuccess) return e;
+    if (k < 1) return cudaErrorInvalidConfiguration;
   }
+  *blocks = k;
+  return cudaSuccess;
+}
+
+template <typename T, int VEC, int EPT, bool WIDE>
+cudaError_t launch_cut(LnParams& p, long long groups, bool bwd, cudaStream_t stream) {
+  if (bwd) {
+    const int threads = 32 * (WIDE ? p.warps : kBwdTeams);
+    p.stages = bwd_smem<T, VEC, EPT, WIDE>(p.warps, p.channels, 2) <= kBwdSmem ? 2 : 1;
+    const size_t smem = bwd_smem<T, VEC, EPT, WIDE>(p.warps, p.channels, p.stages);
+    int blocks = 0;
+    const cudaError_t e = bwd_blocks<T, VEC, EPT, WIDE>(smem, p.warps, &blocks);
+    if (e != cudaSuccess) return e;
+    // as many parts as are resident at once over all groups
+    const long long parts = static_cast<long long>(kSms) * blocks / groups;
+    if (parts < p.parts) p.parts = parts < 1 ? 1 : static_cast<int>(parts);
+    ln_bwd_kernel<T, VEC, EPT, WIDE><<<static_cast<unsigned>(groups * p.parts), threads, smem, stream>>>(p);
+    return cudaGetLastError();
+  }
+  // one warp per block while that still leaves SMs without work, else four
+  const int rows = WIDE || p.rows <= kSms * 8 ? 1 : 4;
+  ln_fwd_kernel<T, VEC, EPT, WIDE><<<static_cast<unsigned>((p.rows + rows - 1) / rows),
+                                     32 * (WIDE ? p.warps : rows), 0, stream>>>(p);
   return cudaGetLastError();
 }
 
+// Elements per lane: the least of the list that covers the row with one warp; wider rows take
+// 32 per lane.
 template <typename T, int VEC>
-cudaError_t launch_width(const LnParams& p, long long groups, bool bwd, cudaStream_t stream) {
-  const int c = p.channels;
-  if (c <= 32 * 8) return launch_team<T, VEC, 32, 8>(p, groups, bwd, stream);
-  if (c <= 32 * 16) return launch_team<T, VEC, 32, 16>(p, groups, bwd, stream);
-  if (c <= 32 * 32) return launch_team<T, VEC, 32, 32>(p, groups, bwd, stream);
-  if (c <= 32 * 48) return launch_team<T, VEC, 32, 48>(p, groups, bwd, stream);
-  if (c <= 128 * 16) return launch_team<T, VEC, 128, 16>(p, groups, bwd, stream);
-  if (c <= 128 * 32) return launch_team<T, VEC, 128, 32>(p, groups, bwd, stream);
-  if (c <= 512 * 16) return launch_team<T, VEC, 512, 16>(p, groups, bwd, stream);
-  return launch_team<T, VEC, 512, 32>(p, groups, bwd, stream);
+cudaError_t launch_width(LnParams& p, long long groups, bool bwd, cudaStream_t stream) {
+  const int per_lane = (p.channels + 31) / 32;
+  p.warps = 1;
+  if (per_lane <= 8) return launch_cut<T, VEC, 8, false>(p, groups, bwd, stream);
+  if (per_lane <= 16) return launch_cut<T, VEC, 16, false>(p, groups, bwd, stream);
+  if (per_lane <= 24) return launch_cut<T, VEC, 24, false>(p, groups, bwd, stream);
+  if (per_lane <= 32) return launch_cut<T, VEC, 32, false>(p, groups, bwd, stream);
+  if (per_lane <= 40) return launch_cut<T, VEC, 40, false>(p, groups, bwd, stream);
+  if (per_lane <= 48) return launch_cut<T, VEC, 48, false>(p, groups, bwd, stream);
+  if (per_lane <= 64) return launch_cut<T, VEC, 64, false>(p, groups, bwd, stream);
+  p.warps = (p.channels + 1023) / 1024;
+  return launch_cut<T, VEC, 32, true>(p, groups, bwd, stream);
 }
 
 template <typename T>
-cudaError_t launch_type(const LnParams& p, long long groups, bool bwd, bool aligned, cudaStream_t stream) {
+cudaError_t launch_type(LnParams& p, long long groups, bool bwd, bool aligned, cudaStream_t stream) {
   constexpr int kVec = 16 / sizeof(T);
   return aligned ? launch_width<T, kVec>(p, groups, bwd, stream) : launch_width<T, 1>(p, groups, bwd, stream);
 }
@@ -325,7 +532,8 @@ bool rows_aligned(const LnArgs& a) {
          ok(a.x) && ok(a.dy) && ok(a.y) && ok(a.weight) && ok(a.bias);
 }
 
-cudaError_t dispatch(const LnArgs& a, const LnParams& p, bool bwd, cudaStream_t stream) {
+// Launches; the backward pass lowers p.parts to what is resident at once.
+cudaError_t dispatch(const LnArgs& a, LnParams& p, bool bwd, cudaStream_t stream) {
   const bool al = rows_aligned(a);
   switch (a.dtype) {
     case PF_BF16: return launch_type<__nv_bfloat16>(p, a.groups, bwd, al, stream);
@@ -356,16 +564,16 @@ LnParams params_of(const LnArgs& a) {
 
 }  // namespace
 
-// Blocks per group of the backward pass: enough for four blocks per SM over all groups, but
-// at least eight rows each, so that a partial row is written once for many rows read.
+// Most blocks per group of the backward pass: each of them has at least eight rows, so that a
+// partial row is written once for many rows read.
 int ln_bwd_parts(long long groups, long long rows_per_group) {
-  long long parts = (148 * 4) / groups;
+  long long parts = kMostParts / groups;
   if (parts > (rows_per_group + 7) / 8) parts = (rows_per_group + 7) / 8;
   return parts < 1 ? 1 : static_cast<int>(parts);
 }
 
 cudaError_t launch_layernorm(const LnArgs& a, cudaStream_t stream) {
-  const LnParams p = params_of(a);
+  LnParams p = params_of(a);
   return p.rows == 0 ? cudaSuccess : dispatch(a, p, false, stream);
 }
 
