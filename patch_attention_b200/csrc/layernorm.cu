@@ -9,11 +9,14 @@
 // Both directions are HBM bound: forward reads x and writes y, backward reads x and dy and
 // writes dx.  A row of up to 2048 elements belongs to one warp, so that it needs no barrier and
 // its fixed cost (two shuffle trees) is spread over up to 64 elements per lane; wider rows belong
-// to a block of up to 16 warps.  The forward pass reads a row into registers once.  The backward
-// pass walks rows: it keeps the weight-gradient sums of a lane's columns in registers, and the
+// to a block of up to 16 warps.  Where a warp has several rows of a group, the group's
+// parameters are converted to fp32 once, into shared memory.  The forward pass reads a row into
+// registers once.  The backward pass keeps the weight-gradient sums of a lane's columns in registers, and the
 // next row of x and dy is copied into shared memory (each lane its own elements, so no barrier)
 // while the current one is worked on.  Arithmetic is on pairs (two fp32 lanes per instruction):
-// element by element, instruction issue was the bound (25 instructions per element forward).
+// element by element, instruction issue was the bound (25 instructions per element forward),
+// as it was with bounds checks on every access: the elements per lane are the least multiple of 8
+// that covers the row, so only a lane's last 8 are checked.
 // The variance is taken around means: a warp's around its own; in wider rows the warps' (mean, sum
 // of squares) are then combined.
 //
@@ -85,15 +88,27 @@ struct Place {
   __device__ __forceinline__ int column(int i) const { return first + i * 32 * VEC; }
 };
 
-// One pair of elements at a time from registers, shared or global memory: U is a unit.
-// Pair k is elements 2k, 2k + 1 of the lane: inside unit 2k / VEC, or (VEC = 1) units 2k, 2k + 1.
 template <typename T, int VEC>
 using Unit = Vec<T, VEC>;
 
-// The lane's parameters of unit group `k` (one unit, or two for VEC = 1) as pairs.
+// How the elements of a lane are walked: K steps, each of P pairs -- one unit, or for VEC = 1 the
+// two units 2k and 2k + 1.
+template <int VEC, int EPT>
+struct Walk {
+  static constexpr int P = VEC == 1 ? 1 : VEC / 2;
+  static constexpr int K = EPT / 2 / P;
+  static constexpr int kPerStep = VEC == 1 ? 2 : 1;
+  // Whether unit i may lie past the row's end; CHECK: every unit may.
+  template <bool CHECK>
+  static __device__ __forceinline__ bool in(int i, const Place<VEC>& at, int n) {
+    return (!CHECK && (i + 1) * VEC <= EPT - 8) || at.column(i) < n;
+  }
+};
+
+// The lane's parameters of step k as pairs, from global memory.
 template <typename T, int VEC, int N>
-__device__ __forceinline__ void unit_params(float2 (&f)[N], const void* base, long long row, float plus, float none,
-                                            int k, const LnParams& p, const Place<VEC>& at) {
+__device__ __forceinline__ void direct_params(float2 (&f)[N], const void* base, long long row, float plus, float none,
+                                              int k, const LnParams& p, const Place<VEC>& at) {
   if constexpr (VEC == 1) {
     float v[2] = {none, none};
 #pragma unroll
@@ -106,32 +121,61 @@ __device__ __forceinline__ void unit_params(float2 (&f)[N], const void* base, lo
       }
     }
     f[0] = make_float2(v[0], v[1]);
+  } else if (base == nullptr) {
+#pragma unroll
+    for (int u = 0; u < VEC / 2; ++u) f[u] = both(none);
+  } else if (p.wide) {
+    float v[VEC];
+    load_param<T, VEC>(base, row + at.column(k), true, v);
+#pragma unroll
+    for (int u = 0; u < VEC / 2; ++u) f[u] = add2(make_float2(v[2 * u], v[2 * u + 1]), both(plus));
   } else {
-    if (base != nullptr) {
-      if (p.wide) {
-        float v[VEC];
-        load_param<T, VEC>(base, row + at.column(k), true, v);
+    const Unit<T, VEC> v = load_vec<T, VEC>(static_cast<const T*>(base) + row + at.column(k));
 #pragma unroll
-        for (int u = 0; u < VEC / 2; ++u) f[u] = add2(make_float2(v[2 * u], v[2 * u + 1]), both(plus));
-      } else {
-        const Unit<T, VEC> v = load_vec<T, VEC>(static_cast<const T*>(base) + row + at.column(k));
-#pragma unroll
-        for (int u = 0; u < VEC / 2; ++u) f[u] = add2(pair_of<T>(v.v + 2 * u), both(plus));
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < VEC / 2; ++u) f[u] = both(none);
-    }
+    for (int u = 0; u < VEC / 2; ++u) f[u] = add2(pair_of<T>(v.v + 2 * u), both(plus));
   }
 }
 
-// How the units of a lane are walked: K groups, each of P pairs.
-template <int VEC, int EPT>
-struct Walk {
-  static constexpr int P = VEC == 1 ? 1 : VEC / 2;
-  static constexpr int K = EPT / 2 / P;
-};
-
+// A group's parameters in shared memory as fp32, so laid out that the lanes of a warp read
+// their 16-byte quarters side by side: [unit][quad of the unit][lane][4] (VEC = 1: in order).
+template <typename T, int VEC>
+__device__ __forceinline__ void stage_params(float* to, const void* base, long long row, float plus, float none,
+                                             const LnParams& p) {
+#pragma unroll 2
+  for (int u = threadIdx.x; u * VEC < p.channels; u += blockDim.x) {
+    float v[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[k] = none;
+    if (base != nullptr) {
+      load_param<T, VEC>(base, row + u * VEC, p.wide, v);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) v[k] += plus;
+    }
+#pragma unroll
+    for (int k = 0; k < VEC; k += 4) {
+      if constexpr (VEC == 1)
+        to[u] = v[0];
+      else
+        *reinterpret_cast<float4*>(to + ((u / 32 * (VEC / 4) + k / 4) * 32 + u % 32) * 4) =
+            make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+    }
+  }
+}
+template <int VEC, int N>
+__device__ __forceinline__ void staged_params(float2 (&f)[N], const float* from, int k, int lane, const Place<VEC>& at,
+                                              int n) {
+  if constexpr (VEC == 1) {
+    f[0].x = from[at.column(2 * k)];
+    f[0].y = at.column(2 * k + 1) < n ? from[at.column(2 * k + 1)] : 0.f;
+  } else {
+#pragma unroll
+    for (int q = 0; q < VEC / 4; ++q) {
+      const float4 v = *reinterpret_cast<const float4*>(from + ((k * (VEC / 4) + q) * 32 + lane) * 4);
+      f[2 * q] = make_float2(v.x, v.y);
+      f[2 * q + 1] = make_float2(v.z, v.w);
+    }
+  }
+}
 // Two values summed over the row's warps.  Consecutive calls alternate between two buffers, so
 // one barrier each is enough.
 struct Exchange {
@@ -146,97 +190,126 @@ struct Exchange {
   }
 };
 
-// Rows of one warp: `blockDim.x / 32` rows per block.  Wider rows (WIDE): one row per block.
-template <typename T, int VEC, int EPT, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 512 : 128) ln_fwd_kernel(const __grid_constant__ LnParams p) {
+// KIND 0: a warp takes one row, parameters from global memory (few rows: least latency).
+// KIND 1: a block of four warps walks rows of one group, its parameters in shared memory.
+// KIND 2: a block of up to 16 warps takes one row.
+template <typename T, int VEC, int EPT, int KIND>
+__global__ void __launch_bounds__(KIND == 2 ? 512 : 128) ln_fwd_kernel(const __grid_constant__ LnParams p) {
   using Wk = Walk<VEC, EPT>;
+  constexpr bool WIDE = KIND == 2;
   __shared__ float2 slots[2][16];
+  __shared__ __align__(16) float staged[KIND == 1 ? 2 * 32 * EPT : 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = WIDE ? blockIdx.x : static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
-  if (row >= p.rows) return;
   const int n = p.channels;
+  long long row, end, g;
+  int step = 1;
+  if constexpr (KIND == 1) {
+    g = blockIdx.x / p.parts;
+    const int part = static_cast<int>(blockIdx.x % p.parts);
+    row = g * p.rows_per_group + p.rows_per_group * part / p.parts + warp;
+    end = g * p.rows_per_group + p.rows_per_group * (part + 1) / p.parts;
+    step = 4;
+    stage_params<T, VEC>(staged, p.weight, g * p.weight_stride, p.w0, 1.f, p);
+    stage_params<T, VEC>(staged + 32 * EPT, p.bias, g * p.bias_stride, 0.f, 0.f, p);
+    __syncthreads();
+  } else {
+    row = KIND == 2 ? blockIdx.x : static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
+    if (row >= p.rows) return;
+    end = row + 1;
+    g = static_cast<unsigned>(row) / static_cast<unsigned>(p.rows_per_group);  // both fit 31 bits
+  }
   const int first = WIDE ? warp * 32 * EPT : 0;  // this warp's columns
   const float mine = static_cast<float>(min(max(n - first, 0), 32 * EPT));
+  const float inv_mine = mine > 0.f ? 1.f / mine : 0.f, inv_n = 1.f / static_cast<float>(n);
   const Place<VEC> at = {first + lane * VEC};
-  const T* x = static_cast<const T*>(p.x) + row * n;
+  if (KIND == 1 && row >= end) return;
   Unit<T, VEC> raw[EPT / VEC];
+  auto fetch = [&](long long r) {
+    const T* x = static_cast<const T*>(p.x) + r * n;
 #pragma unroll
-  for (int i = 0; i < EPT / VEC; ++i)
-    if (at.column(i) < n) raw[i] = load_vec<T, VEC>(x + at.column(i));
-  float2 f[EPT / 2];
-  float2 s2 = both(0.f);
+    for (int i = 0; i < EPT / VEC; ++i)
+      if (Wk::template in<WIDE>(i, at, n)) raw[i] = load_vec<T, VEC>(x + at.column(i));
+  };
+  fetch(row);
+  for (; row < end; row += step) {
+    float2 f[EPT / 2];
+    float2 s2 = both(0.f);
 #pragma unroll
-  for (int k = 0; k < Wk::K; ++k) {
-    if constexpr (VEC == 1) {
-      f[k].x = at.column(2 * k) < n ? to_f<T>(raw[2 * k].v[0]) : 0.f;
-      f[k].y = at.column(2 * k + 1) < n ? to_f<T>(raw[2 * k + 1].v[0]) : 0.f;
-      s2 = add2(s2, f[k]);
-    } else if (at.column(k) < n) {
-#pragma unroll
-      for (int u = 0; u < Wk::P; ++u) {
-        f[k * Wk::P + u] = pair_of<T>(raw[k].v + 2 * u);
-        s2 = add2(s2, f[k * Wk::P + u]);
-      }
-    }
-  }
-  float mean = warp_sum(s2.x + s2.y) * (mine > 0.f ? 1.f / mine : 0.f);
-  float2 q2 = both(0.f);
-#pragma unroll
-  for (int k = 0; k < Wk::K; ++k) {
-    if constexpr (VEC == 1) {
-      float2 d = add2(f[k], both(-mean));
-      if (at.column(2 * k) >= n) d.x = 0.f;
-      if (at.column(2 * k + 1) >= n) d.y = 0.f;
-      q2 = fma2(d, d, q2);
-    } else if (at.column(k) < n) {
-#pragma unroll
-      for (int u = 0; u < Wk::P; ++u) {
-        const float2 d = add2(f[k * Wk::P + u], both(-mean));
-        q2 = fma2(d, d, q2);
-      }
-    }
-  }
-  float sq = warp_sum(q2.x + q2.y);
-  const float inv_n = 1.f / static_cast<float>(n);
-  if constexpr (WIDE) {
-    Exchange ex{slots};
-    const float2* all = ex.publish(make_float2(mean, sq), warp, lane);
-    float m = 0.f, c = 0.f;
-    for (int k = 0; k < p.warps; ++k) m = fmaf(static_cast<float>(min(n - k * 32 * EPT, 32 * EPT)), all[k].x, m);
-    m *= inv_n;
-    for (int k = 0; k < p.warps; ++k) {
-      const float d = all[k].x - m;
-      c += fmaf(static_cast<float>(min(n - k * 32 * EPT, 32 * EPT)) * d, d, all[k].y);
-    }
-    mean = m;
-    sq = c;
-  }
-  const float rstd = rsqrtf(fmaf(sq, inv_n, p.eps));
-  if (lane == 0 && (!WIDE || warp == 0)) {
-    if (p.mean != nullptr) p.mean[row] = mean;
-    if (p.rstd != nullptr) p.rstd[row] = rstd;
-  }
-  // row and rows_per_group fit 31 bits
-  const long long g = static_cast<unsigned>(row) / static_cast<unsigned>(p.rows_per_group);
-  T* y = static_cast<T*>(p.y) + row * n;
-#pragma unroll
-  for (int k = 0; k < Wk::K; ++k) {
-    if (at.column(VEC == 1 ? 2 * k : k) >= n) continue;
-    float2 w[Wk::P], b[Wk::P];
-    unit_params<T, VEC>(w, p.weight, g * p.weight_stride, p.w0, 1.f, k, p, at);
-    unit_params<T, VEC>(b, p.bias, g * p.bias_stride, 0.f, 0.f, k, p, at);
-    Unit<T, VEC> o;
-#pragma unroll
-    for (int u = 0; u < Wk::P; ++u) {
-      const float2 v = fma2(mul2(add2(f[k * Wk::P + u], both(-mean)), both(rstd)), w[u], b[u]);
+    for (int k = 0; k < Wk::K; ++k) {
       if constexpr (VEC == 1) {
-        y[at.column(2 * k)] = from_f<T>(v.x);
-        if (at.column(2 * k + 1) < n) y[at.column(2 * k + 1)] = from_f<T>(v.y);
-      } else {
-        put_pair<T>(o.v + 2 * u, v);
+        f[k].x = Wk::template in<WIDE>(2 * k, at, n) ? to_f<T>(raw[2 * k].v[0]) : 0.f;
+        f[k].y = Wk::template in<WIDE>(2 * k + 1, at, n) ? to_f<T>(raw[2 * k + 1].v[0]) : 0.f;
+        s2 = add2(s2, f[k]);
+      } else if (Wk::template in<WIDE>(k, at, n)) {
+#pragma unroll
+        for (int u = 0; u < Wk::P; ++u) {
+          f[k * Wk::P + u] = pair_of<T>(raw[k].v + 2 * u);
+          s2 = add2(s2, f[k * Wk::P + u]);
+        }
       }
     }
-    if constexpr (VEC > 1) store_vec<T, VEC>(y + at.column(k), o);
+    if (KIND == 1 && row + step < end) fetch(row + step);  // while this row is reduced
+    float mean = warp_sum(s2.x + s2.y) * inv_mine;
+    float2 q2 = both(0.f);
+#pragma unroll
+    for (int k = 0; k < Wk::K; ++k) {
+      if constexpr (VEC == 1) {
+        float2 d = add2(f[k], both(-mean));
+        if (!Wk::template in<WIDE>(2 * k, at, n)) d.x = 0.f;
+        if (!Wk::template in<WIDE>(2 * k + 1, at, n)) d.y = 0.f;
+        q2 = fma2(d, d, q2);
+      } else if (Wk::template in<WIDE>(k, at, n)) {
+#pragma unroll
+        for (int u = 0; u < Wk::P; ++u) {
+          const float2 d = add2(f[k * Wk::P + u], both(-mean));
+          q2 = fma2(d, d, q2);
+        }
+      }
+    }
+    float sq = warp_sum(q2.x + q2.y);
+    if constexpr (WIDE) {
+      Exchange ex{slots};
+      const float2* all = ex.publish(make_float2(mean, sq), warp, lane);
+      float m = 0.f, c = 0.f;
+      for (int k = 0; k < p.warps; ++k) m = fmaf(static_cast<float>(min(n - k * 32 * EPT, 32 * EPT)), all[k].x, m);
+      m *= inv_n;
+      for (int k = 0; k < p.warps; ++k) {
+        const float d = all[k].x - m;
+        c += fmaf(static_cast<float>(min(n - k * 32 * EPT, 32 * EPT)) * d, d, all[k].y);
+      }
+      mean = m;
+      sq = c;
+    }
+    const float rstd = rsqrtf(fmaf(sq, inv_n, p.eps));
+    if (lane == 0 && (!WIDE || warp == 0)) {
+      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    }
+    T* y = static_cast<T*>(p.y) + row * n;
+#pragma unroll
+    for (int k = 0; k < Wk::K; ++k) {
+      if (!Wk::template in<WIDE>(Wk::kPerStep * k, at, n)) continue;
+      float2 w[Wk::P], b[Wk::P];
+      if constexpr (KIND == 1) {
+        staged_params<VEC>(w, staged, k, lane, at, n);
+        staged_params<VEC>(b, staged + 32 * EPT, k, lane, at, n);
+      } else {
+        direct_params<T, VEC>(w, p.weight, g * p.weight_stride, p.w0, 1.f, k, p, at);
+        direct_params<T, VEC>(b, p.bias, g * p.bias_stride, 0.f, 0.f, k, p, at);
+      }
+      Unit<T, VEC> o;
+#pragma unroll
+      for (int u = 0; u < Wk::P; ++u) {
+        const float2 v = fma2(mul2(add2(f[k * Wk::P + u], both(-mean)), both(rstd)), w[u], b[u]);
+        if constexpr (VEC == 1) {
+          y[at.column(2 * k)] = from_f<T>(v.x);
+          if (Wk::template in<WIDE>(2 * k + 1, at, n)) y[at.column(2 * k + 1)] = from_f<T>(v.y);
+        } else {
+          put_pair<T>(o.v + 2 * u, v);
+        }
+      }
+      if constexpr (VEC > 1) store_vec<T, VEC>(y + at.column(k), o);
+    }
   }
 }
 
@@ -251,24 +324,28 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
 
 constexpr int kBwdTeams = 4;  // rows in flight per block where a warp takes a row
 
-// Shared bytes: `stages` rows of (x, dy) units per warp, reused for the sums of a block's teams.
+// Shared bytes: `stages` rows of (x, dy) units per warp, reused for the sums of a block's teams,
+// and (where a warp takes a row) the group's weights.
 // Single 16-bit elements are not staged: a copy into shared memory is at least 4 bytes.
 constexpr size_t kBwdSmem = 200 * 1024;
 template <typename T, int VEC, int EPT, bool WIDE>
-size_t bwd_smem(int warps, int channels, int stages) {
+size_t bwd_smem(int warps, int stages) {
   const size_t row = sizeof(T) * VEC < 4 ? 0 : 2 * EPT * 32 * sizeof(T);
   const size_t ring = (WIDE ? warps : kBwdTeams) * stages * row;
-  const size_t sums = WIDE ? 0 : 2 * static_cast<size_t>(channels) * sizeof(float);
-  return ring > sums ? ring : sums;
+  const size_t sums = WIDE ? 0 : 2 * 32 * EPT * sizeof(float);
+  return (WIDE ? 0 : 32 * EPT * sizeof(float)) + (ring > sums ? ring : sums);
 }
 
 template <typename T, int VEC, int EPT, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_kernel(const __grid_constant__ LnParams p) {
+__global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : EPT <= 16 ? 5 : EPT <= 24 ? 4 : EPT <= 32 ? 3 : 2)
+ln_bwd_kernel(const __grid_constant__ LnParams p) {
   using Wk = Walk<VEC, EPT>;
   // else elements are read from global memory, and again in the second pass over the row
   constexpr bool kRing = sizeof(T) * VEC >= 4;
   constexpr int kUnits = EPT / VEC;
-  extern __shared__ __align__(16) uint8_t dyn[];
+  extern __shared__ __align__(16) uint8_t shared[];
+  float* staged = reinterpret_cast<float*>(shared);
+  uint8_t* dyn = shared + (WIDE ? 0 : 32 * EPT * sizeof(float));
   __shared__ float2 slots[2][16];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Exchange ex{slots};
@@ -290,7 +367,7 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_kernel(const __grid_c
     if constexpr (kRing) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i)
-        if (at.column(i) < n) {
+        if (Wk::template in<WIDE>(i, at, n)) {
           copy_async<sizeof(T) * VEC>(slot(stage, 0, i), x + row * n + at.column(i));
           copy_async<sizeof(T) * VEC>(slot(stage, 1, i), dy + row * n + at.column(i));
         }
@@ -300,6 +377,16 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_kernel(const __grid_c
   float2 aw[EPT / 2], ab[EPT / 2];
 #pragma unroll
   for (int k = 0; k < EPT / 2; ++k) aw[k] = ab[k] = both(0.f);
+  if constexpr (!WIDE) {
+    stage_params<T, VEC>(staged, p.weight, g * p.weight_stride, p.w0, 1.f, p);
+    __syncthreads();
+  }
+  auto weights = [&](float2(&w)[Wk::P], int k) {
+    if constexpr (WIDE)
+      direct_params<T, VEC>(w, p.weight, g * p.weight_stride, p.w0, 1.f, k, p, at);
+    else
+      staged_params<VEC>(w, staged, k, lane, at, n);
+  };
   long long row = lo + (WIDE ? 0 : warp);
   if (row < hi) {
     fetch(row, 0);
@@ -320,13 +407,14 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_kernel(const __grid_c
         else
           asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
-      // pairs of the row's x (which = 0) or dy (1) in unit group k, 0 past the end
+      // pairs of the row's x (which = 0) or dy (1) in step k, a second element past the end as 0
       auto get = [&](int which, int k, float2(&f)[Wk::P]) {
         if constexpr (VEC == 1) {
           const T* src = which ? dy : x;
-          const int c0 = at.column(2 * k), c1 = at.column(2 * k + 1);
-          f[0].x = c0 < n ? to_f<T>(kRing ? slot(stage, which, 2 * k)->v[0] : src[row * n + c0]) : 0.f;
-          f[0].y = c1 < n ? to_f<T>(kRing ? slot(stage, which, 2 * k + 1)->v[0] : src[row * n + c1]) : 0.f;
+          f[0].x = to_f<T>(kRing ? slot(stage, which, 2 * k)->v[0] : src[row * n + at.column(2 * k)]);
+          f[0].y = 0.f;
+          if (Wk::template in<WIDE>(2 * k + 1, at, n))
+            f[0].y = to_f<T>(kRing ? slot(stage, which, 2 * k + 1)->v[0] : src[row * n + at.column(2 * k + 1)]);
         } else {
           const Unit<T, VEC> v = *slot(stage, which, k);
 #pragma unroll
@@ -337,11 +425,11 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_kernel(const __grid_c
       float2 s2 = both(0.f), q2 = both(0.f);
 #pragma unroll
       for (int k = 0; k < Wk::K; ++k) {
-        if (at.column(VEC == 1 ? 2 * k : k) >= n) continue;
+        if (!Wk::template in<WIDE>(Wk::kPerStep * k, at, n)) continue;
         float2 xv[Wk::P], dv[Wk::P], w[Wk::P];
         get(0, k, xv);
         get(1, k, dv);
-        unit_params<T, VEC>(w, p.weight, g * p.weight_stride, p.w0, 1.f, k, p, at);
+        weights(w, k);
 #pragma unroll
         for (int u = 0; u < Wk::P; ++u) {
           const int e = k * Wk::P + u;
@@ -366,11 +454,11 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_kernel(const __grid_c
       T* out = static_cast<T*>(p.y) + row * n;
 #pragma unroll
       for (int k = 0; k < Wk::K; ++k) {
-        if (at.column(VEC == 1 ? 2 * k : k) >= n) continue;
+        if (!Wk::template in<WIDE>(Wk::kPerStep * k, at, n)) continue;
         float2 xv[Wk::P], dv[Wk::P], w[Wk::P];
         get(0, k, xv);
         get(1, k, dv);
-        unit_params<T, VEC>(w, p.weight, g * p.weight_stride, p.w0, 1.f, k, p, at);
+        weights(w, k);
         Unit<T, VEC> o;
 #pragma unroll
         for (int u = 0; u < Wk::P; ++u) {
@@ -378,7 +466,7 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_kernel(const __grid_c
           const float2 v = fma2(xh, c1, fma2(mul2(dv[u], w[u]), both(rstd), c0));
           if constexpr (VEC == 1) {
             out[at.column(2 * k)] = from_f<T>(v.x);
-            if (at.column(2 * k + 1) < n) out[at.column(2 * k + 1)] = from_f<T>(v.y);
+            if (Wk::template in<WIDE>(2 * k + 1, at, n)) out[at.column(2 * k + 1)] = from_f<T>(v.y);
           } else {
             put_pair<T>(o.v + 2 * u, v);
           }
@@ -395,24 +483,34 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_kernel(const __grid_c
   if (p.part == nullptr) return;
   // the block's partial: teams add in order, so the result does not depend on timing
   float* out = p.part + (g * p.parts + part) * 2 * n;
-  float* comb = reinterpret_cast<float*>(dyn);
+  float* comb = reinterpret_cast<float*>(dyn);  // [2][32 EPT], quads laid out as the staged weights
   __syncthreads();
   for (int t = 0; t < kStep; ++t) {
     if (WIDE || warp == t) {
+      const bool last = t + 1 == kStep;
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        const int c = at.column(e / VEC) + e % VEC;
-        if (c < n) {
-          float u = e & 1 ? aw[e / 2].y : aw[e / 2].x, v = e & 1 ? ab[e / 2].y : ab[e / 2].x;
-          if (t > 0) {
-            u += comb[c];
-            v += comb[n + c];
+      for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int e = 0; e < EPT; e += VEC == 1 ? 1 : 4) {
+          const float2* sum = which ? ab : aw;
+          if constexpr (VEC == 1) {
+            const int c = at.column(e);
+            if (c >= n) continue;
+            float v = e & 1 ? sum[e / 2].y : sum[e / 2].x;
+            if (t > 0) v += comb[which * 32 * EPT + e * 32 + lane];
+            if (last)
+              out[which * n + c] = v;
+            else
+              comb[which * 32 * EPT + e * 32 + lane] = v;
+          } else {
+            const int c = at.column(e / VEC) + e % VEC;
+            if (c >= n) continue;
+            float4 v = make_float4(sum[e / 2].x, sum[e / 2].y, sum[e / 2 + 1].x, sum[e / 2 + 1].y);
+            float4* mine = reinterpret_cast<float4*>(comb + which * 32 * EPT) + e / 4 * 32 + lane;
+            if (t > 0) v = make_float4(v.x + mine->x, v.y + mine->y, v.z + mine->z, v.w + mine->w);
+            *(last ? reinterpret_cast<float4*>(out + which * n + c) : mine) = v;
           }
-          float* to = t + 1 == kStep ? out : comb;
-          to[c] = u;
-          to[n + c] = v;
         }
-      }
     }
     if (!WIDE) __syncthreads();
   }
@@ -454,6 +552,7 @@ __global__ void __launch_bounds__(32 * kRedLanes) reduce_parts_kernel(const floa
 
 constexpr int kSms = 148;
 constexpr int kMostParts = kSms * 8;
+constexpr int kFwdBlocks = 5;  // blocks of four warps per SM of the forward kernel that walks rows
 
 // Resident blocks per SM of a backward kernel with rows of `warps` warps, looked up once.
 template <typename T, int VEC, int EPT, bool WIDE>
@@ -482,8 +581,8 @@ template <typename T, int VEC, int EPT, bool WIDE>
 cudaError_t launch_cut(LnParams& p, long long groups, bool bwd, cudaStream_t stream) {
   if (bwd) {
     const int threads = 32 * (WIDE ? p.warps : kBwdTeams);
-    p.stages = bwd_smem<T, VEC, EPT, WIDE>(p.warps, p.channels, 2) <= kBwdSmem ? 2 : 1;
-    const size_t smem = bwd_smem<T, VEC, EPT, WIDE>(p.warps, p.channels, p.stages);
+    p.stages = bwd_smem<T, VEC, EPT, WIDE>(p.warps, 2) <= kBwdSmem ? 2 : 1;
+    const size_t smem = bwd_smem<T, VEC, EPT, WIDE>(p.warps, p.stages);
     int blocks = 0;
     const cudaError_t e = bwd_blocks<T, VEC, EPT, WIDE>(smem, p.warps, &blocks);
     if (e != cudaSuccess) return e;
@@ -493,15 +592,22 @@ cudaError_t launch_cut(LnParams& p, long long groups, bool bwd, cudaStream_t str
     ln_bwd_kernel<T, VEC, EPT, WIDE><<<static_cast<unsigned>(groups * p.parts), threads, smem, stream>>>(p);
     return cudaGetLastError();
   }
+  if (!WIDE && p.rows >= kSms * kFwdBlocks * 4 * 4 && p.rows_per_group >= 16) {
+    // at least four rows for each warp that is resident, and for each warp of a group
+    const long long parts = kSms * kFwdBlocks / groups, most = p.rows_per_group / 16;
+    p.parts = static_cast<int>(parts < 1 ? 1 : parts < most ? parts : most);
+    ln_fwd_kernel<T, VEC, EPT, WIDE ? 2 : 1><<<static_cast<unsigned>(groups * p.parts), 128, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
   // one warp per block while that still leaves SMs without work, else four
   const int rows = WIDE || p.rows <= kSms * 8 ? 1 : 4;
-  ln_fwd_kernel<T, VEC, EPT, WIDE><<<static_cast<unsigned>((p.rows + rows - 1) / rows),
-                                     32 * (WIDE ? p.warps : rows), 0, stream>>>(p);
+  ln_fwd_kernel<T, VEC, EPT, WIDE ? 2 : 0><<<static_cast<unsigned>((p.rows + rows - 1) / rows),
+                                             32 * (WIDE ? p.warps : rows), 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-// Elements per lane: the least of the list that covers the row with one warp; wider rows take
-// 32 per lane.
+// Elements per lane: the least multiple of 8 that covers the row with one warp; rows that
+// would take more than 64 take 32 per lane of several warps.
 template <typename T, int VEC>
 cudaError_t launch_width(LnParams& p, long long groups, bool bwd, cudaStream_t stream) {
   const int per_lane = (p.channels + 31) / 32;
@@ -512,6 +618,7 @@ cudaError_t launch_width(LnParams& p, long long groups, bool bwd, cudaStream_t s
   if (per_lane <= 32) return launch_cut<T, VEC, 32, false>(p, groups, bwd, stream);
   if (per_lane <= 40) return launch_cut<T, VEC, 40, false>(p, groups, bwd, stream);
   if (per_lane <= 48) return launch_cut<T, VEC, 48, false>(p, groups, bwd, stream);
+  if (per_lane <= 56) return launch_cut<T, VEC, 56, false>(p, groups, bwd, stream);
   if (per_lane <= 64) return launch_cut<T, VEC, 64, false>(p, groups, bwd, stream);
   p.warps = (p.channels + 1023) / 1024;
   return launch_cut<T, VEC, 32, true>(p, groups, bwd, stream);
