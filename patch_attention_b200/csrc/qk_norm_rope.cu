@@ -10,13 +10,14 @@
 // HBM bound: every element is read once and written once (backward: two reads, one write).
 // A lane owns four pairs of a vector, so a pair's elements meet in one lane's registers for
 // either pairing: one 16-byte access for interleaved pairs (e1 = e0 + 1), two 8-byte ones for
-// half-split pairs (e1 = e0 + w_a / 2).  The four angles of a lane are the same for every
-// head of a token: a warp takes one token (or a share of its heads) and computes them once.
-// Angles are taken in turns, pos * (theta^(-2i/w) / 2 pi) in 64 bits, and only their fraction
-// is rounded to 32 bits, so far positions lose nothing.
+// half-split pairs (e1 = e0 + w_a / 2).  A block takes 1 to 8 tokens; its threads first compute the
+// tokens' cosines and sines once, into shared memory (behind the first loads), then each warp
+// walks its share of a token's heads, 32 / SEG vectors at a time with kUnroll steps of loads in
+// flight.  Angles are taken in turns, pos * (theta^(-2i/w) / 2 pi) in 64 bits, and only their
+// fraction is rounded to 32 bits, so far positions lose nothing.
 //
-// The backward pass keeps the gain-gradient sums of a lane's elements in registers over the
-// tokens of its warp; blocks write fp32 partials that a second kernel adds in a fixed order.
+// The backward pass keeps the gain-gradient sums of a lane's elements in registers while its
+// block walks tokens; blocks write fp32 partials that a second kernel adds in a fixed order.
 
 #include "block_ops.cuh"
 
@@ -36,80 +37,79 @@ struct RopeParams {
   const float* pos;   // [tokens][n_axes] (pos_batch apart per batch element)
   long long pos_batch;
   float* part;        // backward: [block][2][head_dim], or null
-  long long items;    // batch * tokens * splits
-  int tokens, n_axes, heads[2], head_dim, splits;
+  int total;          // batch * tokens
+  int tokens, n_axes, heads[2], head_dim;
+  int shares;         // warps of a block that share a token's heads: 1, 2, 4 or 8
   float eps;          // 0: no norm
   RopeTable tab;
 };
 
-// A lane's four pairs: where they lie and how far they turn per unit of position.
-struct Pairs {
-  float c[4], s[4];
-  bool turn[4];
+// A lane's eight elements as read: one run (INTER) or PV-element pieces of both halves.
+template <typename T, bool INTER, int PV>
+struct Raw {
+  Vec<T, INTER ? 8 : PV> v[INTER ? 1 : 8 / PV];
+
+  __device__ __forceinline__ void load(const T* p, const int (&e0)[4], const int (&e1)[4]) {
+    if constexpr (INTER) {
+      v[0] = load_vec<T, 8>(p + e0[0]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; k += PV) {
+        v[k / PV] = load_vec<T, PV>(p + e0[k]);
+        v[4 / PV + k / PV] = load_vec<T, PV>(p + e1[k]);
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (INTER ? 1 : 8 / PV); ++i)
+#pragma unroll
+      for (int k = 0; k < (INTER ? 8 : PV); ++k) v[i].v[k] = from_f<T>(0.f);
+  }
+  __device__ __forceinline__ void store(T* p, const int (&e0)[4], const int (&e1)[4]) const {
+    if constexpr (INTER) {
+      store_vec<T, 8>(p + e0[0], v[0]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; k += PV) {
+        store_vec<T, PV>(p + e0[k], v[k / PV]);
+        store_vec<T, PV>(p + e1[k], v[4 / PV + k / PV]);
+      }
+    }
+  }
+  // first and second elements of the four pairs
+  __device__ __forceinline__ void get(float (&a)[4], float (&b)[4]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = to_f<T>(INTER ? v[0].v[2 * k] : v[k / PV].v[k % PV]);
+      b[k] = to_f<T>(INTER ? v[0].v[2 * k + 1] : v[4 / PV + k / PV].v[k % PV]);
+    }
+  }
+  __device__ __forceinline__ void put(const float (&a)[4], const float (&b)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      (INTER ? v[0].v[2 * k] : v[k / PV].v[k % PV]) = from_f<T>(a[k]);
+      (INTER ? v[0].v[2 * k + 1] : v[4 / PV + k / PV].v[k % PV]) = from_f<T>(b[k]);
+    }
+  }
 };
 
-// Elements of a lane's pairs, first[k] and second[k], as PV consecutive ones per access.
-// INTER: pair k is elements (e + 2 k, e + 2 k + 1) of one 8-element run.
-template <typename T, bool INTER, int PV>
-__device__ __forceinline__ void load8(const T* p, const int (&e0)[4], const int (&e1)[4], float (&a)[4], float (&b)[4]) {
-  if constexpr (INTER) {
-    const auto v = load_vec<T, 8>(p + e0[0]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      a[k] = to_f<T>(v.v[2 * k]);
-      b[k] = to_f<T>(v.v[2 * k + 1]);
+// cos and sin of every pair of the block's tokens, [token of the block][pair].
+__device__ __forceinline__ void fill_angles(const RopeParams& p, float2* cs, unsigned first, int count) {
+  const int pairs = p.head_dim / 2;
+  for (int i = threadIdx.x; i < count * pairs; i += 32 * kWarps) {
+    const int t = i / pairs, k = i - t * pairs;
+    const unsigned bt = first + t;
+    if (bt >= static_cast<unsigned>(p.total)) break;
+    const unsigned b = bt / static_cast<unsigned>(p.tokens), tok = bt - b * static_cast<unsigned>(p.tokens);
+    const int axis = p.tab.axis[k];
+    float c = 1.f, s = 0.f;
+    if (axis < p.n_axes) {
+      const float at = __ldg(p.pos + b * p.pos_batch + static_cast<long long>(tok) * p.n_axes + axis);
+      const double turns = static_cast<double>(at) * p.tab.turns[k];
+      sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; k += PV) {
-      const auto u = load_vec<T, PV>(p + e0[k]);
-      const auto v = load_vec<T, PV>(p + e1[k]);
-#pragma unroll
-      for (int j = 0; j < PV; ++j) {
-        a[k + j] = to_f<T>(u.v[j]);
-        b[k + j] = to_f<T>(v.v[j]);
-      }
-    }
-  }
-}
-
-template <typename T, bool INTER, int PV>
-__device__ __forceinline__ void store8(T* p, const int (&e0)[4], const int (&e1)[4], const float (&a)[4], const float (&b)[4]) {
-  if constexpr (INTER) {
-    Vec<T, 8> v;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v.v[2 * k] = from_f<T>(a[k]);
-      v.v[2 * k + 1] = from_f<T>(b[k]);
-    }
-    store_vec<T, 8>(p + e0[0], v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; k += PV) {
-      Vec<T, PV> u, v;
-#pragma unroll
-      for (int j = 0; j < PV; ++j) {
-        u.v[j] = from_f<T>(a[k + j]);
-        v.v[j] = from_f<T>(b[k + j]);
-      }
-      store_vec<T, PV>(p + e0[k], u);
-      store_vec<T, PV>(p + e1[k], v);
-    }
-  }
-}
-
-__device__ __forceinline__ void token_angles(const RopeParams& p, int lane_pair0, const float* pos, Pairs& pr) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = lane_pair0 + k;
-    const int axis = p.tab.axis[i];
-    pr.turn[k] = axis < p.n_axes;  // pairs past the axes are copied
-    pr.c[k] = 1.f;
-    pr.s[k] = 0.f;
-    if (pr.turn[k]) {
-      const double turns = static_cast<double>(__ldg(pos + axis)) * p.tab.turns[i];
-      sincospif(2.f * static_cast<float>(turns - rint(turns)), &pr.s[k], &pr.c[k]);
-    }
+    cs[t * 128 + k] = make_float2(c, s);
   }
 }
 
@@ -120,181 +120,231 @@ __device__ __forceinline__ float seg_sum(float v) {
   return v;
 }
 
-// The heads of a warp's item are walked 32 / SEG at a time, kUnroll steps of loads in flight.
+// This warp's token and heads of a block's tokens.
+struct Item {
+  unsigned b, tok;
+  int slot, lo, hi;  // token of the block; heads [lo, hi) of q's and k's together
+  bool on;
+  __device__ Item(const RopeParams& p, unsigned first, int warp, int split, int splits) {
+    slot = warp / p.shares;
+    const unsigned bt = first + slot;
+    on = bt < static_cast<unsigned>(p.total);
+    b = bt / static_cast<unsigned>(p.tokens);
+    tok = bt - b * static_cast<unsigned>(p.tokens);
+    const int n = p.heads[0] + p.heads[1], share = split * p.shares + warp % p.shares, all = splits * p.shares;
+    lo = static_cast<int>(static_cast<long long>(n) * share / all);
+    hi = static_cast<int>(static_cast<long long>(n) * (share + 1) / all);
+  }
+};
+
+// A lane's place in a vector.
+struct Lane {
+  int sub, e0[4], e1[4], pair0;
+  bool active;
+  unsigned turn;  // bit k: pair k turns (pairs past the axes are copied)
+  template <int SEG>
+  static __device__ __forceinline__ Lane make(const RopeParams& p) {
+    Lane l;
+    const int lane = threadIdx.x & 31, chunk = lane % SEG;
+    l.sub = lane / SEG;
+    l.active = chunk * 8 < p.head_dim;
+    l.pair0 = l.active ? chunk * 4 : 0;
+    l.turn = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      l.e0[k] = p.tab.e0[l.pair0 + k];
+      l.e1[k] = p.tab.e1[l.pair0 + k];
+      l.turn |= (p.tab.axis[l.pair0 + k] < p.n_axes ? 1u : 0u) << k;
+    }
+    return l;
+  }
+};
+
 template <typename T, bool INTER, int PV, int SEG>
 __global__ void __launch_bounds__(32 * kWarps) rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPer = 32 / SEG;
   constexpr int kUnroll = 4;
-  const int lane = threadIdx.x & 31, sub = lane / SEG, chunk = lane % SEG;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (item >= p.items) return;  // whole warps leave
-  const int split = static_cast<int>(item % p.splits);
-  const long long bt = item / p.splits;
-  const long long b = bt / p.tokens, tok = bt % p.tokens;
-  const bool active = chunk * 8 < p.head_dim;
-  const int i0 = active ? chunk * 4 : 0;
-  int e0[4], e1[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    e0[k] = p.tab.e0[i0 + k];
-    e1[k] = p.tab.e1[i0 + k];
-  }
-  const int n = p.heads[0] + p.heads[1];
-  const int h_lo = n * split / p.splits, h_hi = n * (split + 1) / p.splits;
-  float ga[2][4], gb[2][4];
+  __shared__ float2 cs[kWarps * 128];
+  const Lane ln = Lane::make<SEG>(p);
+  const int per_block = kWarps / p.shares;
+  const unsigned first = blockIdx.x * static_cast<unsigned>(per_block);
+  const Item it(p, first, threadIdx.x >> 5, blockIdx.y, gridDim.y);
+  const float inv_d = 1.f / static_cast<float>(p.head_dim);
+  const bool norm = p.eps > 0.f;
+  bool filled = false;
+  float c[4], s[4];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
+    const int lo = w ? max(it.lo - p.heads[0], 0) : it.lo, hi = w ? it.hi - p.heads[0] : min(it.hi, p.heads[0]);
+    if (w == 1 && (!it.on || lo >= hi)) break;
+    const bool any = it.on && lo < hi;
+    const T* x = static_cast<const T*>(p.x[w]) + it.b * p.xs[w][0] + it.tok * p.xs[w][1];
+    T* y = static_cast<T*>(p.y[w]) + it.b * p.ys[w][0] + it.tok * p.ys[w][1];
+    float ga[4], gb[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) ga[w][k] = gb[w][k] = 1.f;
-    if (p.gain[w] != nullptr) load8<T, INTER, PV>(static_cast<const T*>(p.gain[w]), e0, e1, ga[w], gb[w]);
-  }
-  Pairs pr;
-  bool angles = false;
-  const float inv_d = 1.f / static_cast<float>(p.head_dim);
-  for (int h0 = h_lo; h0 < h_hi; h0 += kPer * kUnroll) {
-    float a[kUnroll][4], c[kUnroll][4];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * kPer + sub;
-      const int w = h >= p.heads[0];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) a[u][k] = c[u][k] = 0.f;
-      if (active && h < h_hi)
-        load8<T, INTER, PV>(static_cast<const T*>(p.x[w]) + b * p.xs[w][0] + tok * p.xs[w][1] +
-                                (h - w * p.heads[0]) * p.xs[w][2],
-                            e0, e1, a[u], c[u]);
+    for (int k = 0; k < 4; ++k) ga[k] = gb[k] = 1.f;
+    if (any && p.gain[w] != nullptr) {
+      Raw<T, INTER, PV> g;
+      g.load(static_cast<const T*>(p.gain[w]), ln.e0, ln.e1);
+      g.get(ga, gb);
     }
-    if (!angles) {  // behind the first loads
-      token_angles(p, i0, p.pos + b * p.pos_batch + tok * p.n_axes, pr);
-      angles = true;
-    }
-    float r[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) r[u] = 1.f;
-    if (p.eps > 0.f) {
+    for (int h0 = lo; h0 < hi || !filled; h0 += kPer * kUnroll) {
+      Raw<T, INTER, PV> raw[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        float ss = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) ss = fmaf(a[u][k], a[u][k], fmaf(c[u][k], c[u][k], ss));
-        r[u] = rsqrtf(fmaf(seg_sum<SEG>(ss), inv_d, p.eps));
+        const int h = h0 + u * kPer + ln.sub;
+        if (any && ln.active && h < hi)
+          raw[u].load(x + h * p.xs[w][2], ln.e0, ln.e1);
+        else
+          raw[u].zero();
       }
-    }
+      if (!filled) {
+        fill_angles(p, cs, first, per_block);
+        __syncthreads();
+        filled = true;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * kPer + sub;
-      const int w = h >= p.heads[0];
-      if (!active || h >= h_hi) continue;
-      float ya[4], yb[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float za = a[u][k] * r[u] * (w ? ga[1][k] : ga[0][k]);
-        const float zb = c[u][k] * r[u] * (w ? gb[1][k] : gb[0][k]);
-        ya[k] = pr.turn[k] ? za * pr.c[k] - zb * pr.s[k] : za;
-        yb[k] = pr.turn[k] ? za * pr.s[k] + zb * pr.c[k] : zb;
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = cs[it.slot * 128 + ln.pair0 + k];
+          c[k] = v.x;
+          s[k] = v.y;
+        }
       }
-      store8<T, INTER, PV>(static_cast<T*>(p.y[w]) + b * p.ys[w][0] + tok * p.ys[w][1] +
-                               (h - w * p.heads[0]) * p.ys[w][2],
-                           e0, e1, ya, yb);
+      float a[kUnroll][4], b[kUnroll][4], r[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        raw[u].get(a[u], b[u]);
+        r[u] = 1.f;
+      }
+      if (norm) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          float ss = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ss = fmaf(a[u][k], a[u][k], fmaf(b[u][k], b[u][k], ss));
+          r[u] = rsqrtf(fmaf(seg_sum<SEG>(ss), inv_d, p.eps));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int h = h0 + u * kPer + ln.sub;
+        float ya[4], yb[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float za = a[u][k] * (r[u] * ga[k]), zb = b[u][k] * (r[u] * gb[k]);
+          const bool turn = ln.turn >> k & 1u;
+          ya[k] = turn ? za * c[k] - zb * s[k] : za;
+          yb[k] = turn ? za * s[k] + zb * c[k] : zb;
+        }
+        raw[u].put(ya, yb);
+        if (any && ln.active && h < hi) raw[u].store(y + h * p.ys[w][2], ln.e0, ln.e1);
+      }
     }
   }
 }
 
 template <typename T, bool INTER, int PV, int SEG>
-__global__ void __launch_bounds__(32 * kWarps) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 2) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPer = 32 / SEG;
   constexpr int kUnroll = 2;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float2 cs[2][kWarps * 128];
   __shared__ float red[2][256];
-  const int lane = threadIdx.x & 31, sub = lane / SEG, chunk = lane % SEG, warp = threadIdx.x >> 5;
-  const bool active = chunk * 8 < p.head_dim;
-  const int i0 = active ? chunk * 4 : 0;
-  int e0[4], e1[4];
+  const Lane ln = Lane::make<SEG>(p);
+  const int warp = threadIdx.x >> 5;
+  const int per_block = kWarps / p.shares;
+  float sa[2][4], sb[2][4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    e0[k] = p.tab.e0[i0 + k];
-    e1[k] = p.tab.e1[i0 + k];
-  }
-  float ga[2][4], gb[2][4], sa[2][4], sb[2][4];
+  for (int w = 0; w < 2; ++w)
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      ga[w][k] = gb[w][k] = 1.f;
-      sa[w][k] = sb[w][k] = 0.f;
-    }
-    if (p.gain[w] != nullptr) load8<T, INTER, PV>(static_cast<const T*>(p.gain[w]), e0, e1, ga[w], gb[w]);
-  }
-  const int n = p.heads[0] + p.heads[1];
+    for (int k = 0; k < 4; ++k) sa[w][k] = sb[w][k] = 0.f;
   const float inv_d = 1.f / static_cast<float>(p.head_dim);
   const bool norm = p.eps > 0.f;
-  const long long stride = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long item = static_cast<long long>(blockIdx.x) * kWarps + warp; item < p.items; item += stride) {
-    const int split = static_cast<int>(item % p.splits);
-    const long long bt = item / p.splits;
-    const long long b = bt / p.tokens, tok = bt % p.tokens;
-    const int h_lo = n * split / p.splits, h_hi = n * (split + 1) / p.splits;
-    Pairs pr;
-    token_angles(p, i0, p.pos + b * p.pos_batch + tok * p.n_axes, pr);
-    for (int h0 = h_lo; h0 < h_hi; h0 += kPer * kUnroll) {
-      float a[kUnroll][4], c[kUnroll][4], da[kUnroll][4], db[kUnroll][4];
+  const unsigned stride = gridDim.x * static_cast<unsigned>(per_block);
+  int buf = 0;
+  for (unsigned first = blockIdx.x * static_cast<unsigned>(per_block); first < static_cast<unsigned>(p.total);
+       first += stride, buf ^= 1) {
+    const Item it(p, first, warp, 0, 1);
+    bool filled = false;
+    float c[4], s[4];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = h0 + u * kPer + sub;
-        const int w = h >= p.heads[0];
-        const long long hh = h - w * p.heads[0];
+    for (int w = 0; w < 2; ++w) {
+      const int lo = w ? max(it.lo - p.heads[0], 0) : it.lo, hi = w ? it.hi - p.heads[0] : min(it.hi, p.heads[0]);
+      if (w == 1 && (!it.on || lo >= hi)) break;
+      const bool any = it.on && lo < hi;
+      const T* x = static_cast<const T*>(p.x[w]) + it.b * p.xs[w][0] + it.tok * p.xs[w][1];
+      const T* d = static_cast<const T*>(p.dy[w]) + it.b * p.ds[w][0] + it.tok * p.ds[w][1];
+      T* y = static_cast<T*>(p.y[w]) + it.b * p.ys[w][0] + it.tok * p.ys[w][1];
+      float ga[4], gb[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) a[u][k] = c[u][k] = da[u][k] = db[u][k] = 0.f;
-        if (active && h < h_hi) {
-          load8<T, INTER, PV>(static_cast<const T*>(p.dy[w]) + b * p.ds[w][0] + tok * p.ds[w][1] + hh * p.ds[w][2],
-                              e0, e1, da[u], db[u]);
-          if (norm)
-            load8<T, INTER, PV>(static_cast<const T*>(p.x[w]) + b * p.xs[w][0] + tok * p.xs[w][1] + hh * p.xs[w][2],
-                                e0, e1, a[u], c[u]);
-        }
+      for (int k = 0; k < 4; ++k) ga[k] = gb[k] = 1.f;
+      if (any && p.gain[w] != nullptr) {
+        Raw<T, INTER, PV> g;
+        g.load(static_cast<const T*>(p.gain[w]), ln.e0, ln.e1);
+        g.get(ga, gb);
       }
+      for (int h0 = lo; h0 < hi || !filled; h0 += kPer * kUnroll) {
+        Raw<T, INTER, PV> rd[kUnroll], rx[kUnroll];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = h0 + u * kPer + sub;
-        const int w = h >= p.heads[0];
-        float za[4], zb[4], ss = 0.f, sx = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          za[k] = pr.turn[k] ? da[u][k] * pr.c[k] + db[u][k] * pr.s[k] : da[u][k];
-          zb[k] = pr.turn[k] ? db[u][k] * pr.c[k] - da[u][k] * pr.s[k] : db[u][k];
-        }
-        if (norm) {
-          float ta[4], tb[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            ta[k] = za[k] * (w ? ga[1][k] : ga[0][k]);
-            tb[k] = zb[k] * (w ? gb[1][k] : gb[0][k]);
-            ss = fmaf(a[u][k], a[u][k], fmaf(c[u][k], c[u][k], ss));
-            sx = fmaf(ta[k], a[u][k], fmaf(tb[k], c[u][k], sx));
+        for (int u = 0; u < kUnroll; ++u) {
+          const int h = h0 + u * kPer + ln.sub;
+          rd[u].zero();
+          rx[u].zero();
+          if (any && ln.active && h < hi) {
+            rd[u].load(d + h * p.ds[w][2], ln.e0, ln.e1);
+            if (norm) rx[u].load(x + h * p.xs[w][2], ln.e0, ln.e1);
           }
-          ss = seg_sum<SEG>(ss);
-          sx = seg_sum<SEG>(sx);
-          const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-          const float m = r * r * sx * inv_d;  // r mean(a x^) = r^2 mean(a x): times x, then r
+        }
+        if (!filled) {
+          // two tables in turn: the barrier of the next tokens also covers this one's readers
+          fill_angles(p, cs[buf], first, per_block);
+          __syncthreads();
+          filled = true;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float xa = a[u][k] * r, xb = c[u][k] * r;
-            // an absent head has dz = x = 0 and adds nothing
-            if (w) {
-              sa[1][k] = fmaf(za[k], xa, sa[1][k]);
-              sb[1][k] = fmaf(zb[k], xb, sb[1][k]);
-            } else {
-              sa[0][k] = fmaf(za[k], xa, sa[0][k]);
-              sb[0][k] = fmaf(zb[k], xb, sb[0][k]);
+            const float2 v = cs[buf][it.slot * 128 + ln.pair0 + k];
+            c[k] = v.x;
+            s[k] = v.y;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int h = h0 + u * kPer + ln.sub;
+          float da[4], db[4], za[4], zb[4];
+          rd[u].get(da, db);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const bool turn = ln.turn >> k & 1u;
+            za[k] = turn ? da[k] * c[k] + db[k] * s[k] : da[k];
+            zb[k] = turn ? db[k] * c[k] - da[k] * s[k] : db[k];
+          }
+          if (norm) {
+            float a[4], b[4], ta[4], tb[4], ss = 0.f, sx = 0.f;
+            rx[u].get(a, b);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              ta[k] = za[k] * ga[k];
+              tb[k] = zb[k] * gb[k];
+              ss = fmaf(a[k], a[k], fmaf(b[k], b[k], ss));
+              sx = fmaf(ta[k], a[k], fmaf(tb[k], b[k], sx));
             }
-            za[k] = r * (ta[k] - a[u][k] * m);
-            zb[k] = r * (tb[k] - c[u][k] * m);
+            ss = seg_sum<SEG>(ss);
+            sx = seg_sum<SEG>(sx);
+            const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+            const float m = r * r * sx * inv_d;  // r mean(a x^) = r^2 mean(a x): times x, then r
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // an absent head has dz = x = 0 and adds nothing
+              sa[w][k] = fmaf(za[k], a[k] * r, sa[w][k]);
+              sb[w][k] = fmaf(zb[k], b[k] * r, sb[w][k]);
+              za[k] = r * (ta[k] - a[k] * m);
+              zb[k] = r * (tb[k] - b[k] * m);
+            }
+          }
+          if (any && ln.active && h < hi) {
+            rd[u].put(za, zb);
+            rd[u].store(y + h * p.ys[w][2], ln.e0, ln.e1);
           }
         }
-        if (active && h < h_hi)
-          store8<T, INTER, PV>(static_cast<T*>(p.y[w]) + b * p.ys[w][0] + tok * p.ys[w][1] +
-                                   (h - w * p.heads[0]) * p.ys[w][2],
-                               e0, e1, za, zb);
       }
     }
   }
@@ -311,13 +361,13 @@ __global__ void __launch_bounds__(32 * kWarps) rope_bwd_kernel(const __grid_cons
       }
     }
   for (int wi = 0; wi < kWarps; ++wi) {
-    if (warp == wi && sub == 0 && active) {
+    if (warp == wi && ln.sub == 0 && ln.active) {
 #pragma unroll
       for (int w = 0; w < 2; ++w)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          red[w][e0[k]] = wi == 0 ? sa[w][k] : red[w][e0[k]] + sa[w][k];
-          red[w][e1[k]] = wi == 0 ? sb[w][k] : red[w][e1[k]] + sb[w][k];
+          red[w][ln.e0[k]] = wi == 0 ? sa[w][k] : red[w][ln.e0[k]] + sa[w][k];
+          red[w][ln.e1[k]] = wi == 0 ? sb[w][k] : red[w][ln.e1[k]] + sb[w][k];
         }
     }
     __syncthreads();
@@ -328,7 +378,7 @@ __global__ void __launch_bounds__(32 * kWarps) rope_bwd_kernel(const __grid_cons
 }
 
 template <typename T, bool INTER, int PV, int SEG>
-cudaError_t launch_kernel(const RopeParams& p, bool bwd, int blocks, cudaStream_t stream) {
+cudaError_t launch_kernel(const RopeParams& p, bool bwd, dim3 blocks, cudaStream_t stream) {
   if (bwd)
     rope_bwd_kernel<T, INTER, PV, SEG><<<blocks, 32 * kWarps, 0, stream>>>(p);
   else
@@ -337,7 +387,7 @@ cudaError_t launch_kernel(const RopeParams& p, bool bwd, int blocks, cudaStream_
 }
 
 template <typename T, bool INTER, int PV>
-cudaError_t launch_seg(const RopeParams& p, bool bwd, int blocks, cudaStream_t stream) {
+cudaError_t launch_seg(const RopeParams& p, bool bwd, dim3 blocks, cudaStream_t stream) {
   const int chunks = p.head_dim / 8;
   if (chunks <= 4) return launch_kernel<T, INTER, PV, 4>(p, bwd, blocks, stream);
   if (chunks <= 8) return launch_kernel<T, INTER, PV, 8>(p, bwd, blocks, stream);
@@ -346,7 +396,7 @@ cudaError_t launch_seg(const RopeParams& p, bool bwd, int blocks, cudaStream_t s
 }
 
 template <typename T>
-cudaError_t launch_type(const RopeParams& p, bool inter, bool bwd, int blocks, cudaStream_t stream) {
+cudaError_t launch_type(const RopeParams& p, bool inter, bool bwd, dim3 blocks, cudaStream_t stream) {
   if (inter) return launch_seg<T, true, 4>(p, bwd, blocks, stream);
   // half-split pairs: 4, 2 or 1 consecutive elements of a lane's pairs lie side by side,
   // aligned, when every section's half is a multiple of that
@@ -355,7 +405,7 @@ cudaError_t launch_type(const RopeParams& p, bool inter, bool bwd, int blocks, c
   return launch_seg<T, false, 1>(p, bwd, blocks, stream);
 }
 
-cudaError_t dispatch(const RopeArgs& a, const RopeParams& p, bool bwd, int blocks, cudaStream_t stream) {
+cudaError_t dispatch(const RopeArgs& a, const RopeParams& p, bool bwd, dim3 blocks, cudaStream_t stream) {
   switch (a.dtype) {
     case PF_BF16: return launch_type<__nv_bfloat16>(p, a.interleaved, bwd, blocks, stream);
     case PF_F16: return launch_type<__half>(p, a.interleaved, bwd, blocks, stream);
@@ -363,12 +413,28 @@ cudaError_t dispatch(const RopeArgs& a, const RopeParams& p, bool bwd, int block
   }
 }
 
-// A warp takes a whole token, whose angles it then computes once, unless the tokens are too
-// few to give every SM sixteen warps; then a token's heads are shared out.
-int head_splits(long long tokens, int heads, int per_step) {
-  const long long want = (148 * 16 + tokens - 1) / tokens;
-  const long long most = (heads + per_step - 1) / per_step;
-  return static_cast<int>(want < most ? want : most);
+// How a call's tokens and heads are laid over blocks: `shares` warps per token so that the
+// tokens give every SM sixteen warps or more, and, where eight are not enough, the heads of a
+// token over `splits` blocks (forward only).
+struct Grid {
+  int shares, splits, blocks;
+};
+Grid grid_of(const RopeParams& p, bool bwd) {
+  const int chunks = p.head_dim / 8;
+  const int per_step = chunks <= 4 ? 8 : chunks <= 8 ? 4 : chunks <= 16 ? 2 : 1;  // vectors of a warp at once
+  const long long steps = (p.heads[0] + p.heads[1] + per_step - 1) / per_step;    // most warps with work
+  const long long want = (148 * 16 + p.total - 1) / p.total;
+  Grid g = {1, 1, 0};
+  while (g.shares < 8 && g.shares < want && g.shares < steps) g.shares *= 2;
+  if (!bwd && g.shares == 8) {
+    const long long more = want < steps ? want : steps;
+    g.splits = static_cast<int>((more + 7) / 8);
+  }
+  const int per_block = kWarps / g.shares;
+  g.blocks = (p.total + per_block - 1) / per_block;
+  // backward: two blocks per SM walk the tokens, so that few partial gain gradients are written
+  if (bwd && g.blocks > 148 * 2) g.blocks = 148 * 2;
+  return g;
 }
 
 RopeParams params_of(const RopeArgs& a) {
@@ -387,46 +453,44 @@ RopeParams params_of(const RopeArgs& a) {
   }
   p.pos = a.pos;
   p.pos_batch = a.pos_batch;
+  p.total = a.batch * a.tokens;  // at most 2^31 - 1, checked
   p.tokens = a.tokens;
   p.n_axes = a.n_axes;
   p.head_dim = a.head_dim;
   p.eps = a.eps;
   p.tab = a.tab;
-  const int chunks = a.head_dim / 8;
-  const int per_step = chunks <= 4 ? 8 : chunks <= 8 ? 4 : chunks <= 16 ? 2 : 1;
-  const long long toks = static_cast<long long>(a.batch) * a.tokens;
-  p.splits = toks > 0 ? head_splits(toks, a.heads[0] + a.heads[1], per_step) : 1;
-  p.items = toks * p.splits;
   return p;
 }
 
 }  // namespace
 
-// Blocks of the backward pass: at most three per SM, each warp walking several tokens, so
-// that few partial gain gradients are written.
+// Blocks of the backward pass, each writing one partial row of gain gradients.
 int rope_bwd_blocks(const RopeArgs& a) {
-  const long long items = params_of(a).items;
-  const long long blocks = (items + kWarps - 1) / kWarps;
-  return static_cast<int>(blocks < 148 * 3 ? blocks : 148 * 3);
+  const RopeParams p = params_of(a);
+  return p.total == 0 ? 0 : grid_of(p, true).blocks;
 }
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
-  const RopeParams p = params_of(a);
-  if (p.items == 0) return cudaSuccess;
-  return dispatch(a, p, false, static_cast<int>((p.items + kWarps - 1) / kWarps), stream);
+  RopeParams p = params_of(a);
+  if (p.total == 0) return cudaSuccess;
+  const Grid g = grid_of(p, false);
+  p.shares = g.shares;
+  return dispatch(a, p, false, dim3(static_cast<unsigned>(g.blocks), static_cast<unsigned>(g.splits)), stream);
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, void* dgain_q, void* dgain_k, float* part, cudaStream_t stream) {
   RopeParams p = params_of(a);
   const bool sums = dgain_q != nullptr || dgain_k != nullptr;
   p.part = sums ? part : nullptr;
-  const int blocks = rope_bwd_blocks(a);
-  if (blocks > 0) {
-    const cudaError_t e = dispatch(a, p, true, blocks, stream);
+  Grid g = {1, 1, 0};
+  if (p.total > 0) {
+    g = grid_of(p, true);
+    p.shares = g.shares;
+    const cudaError_t e = dispatch(a, p, true, dim3(static_cast<unsigned>(g.blocks)), stream);
     if (e != cudaSuccess) return e;
   }
   if (!sums) return cudaSuccess;
-  return launch_reduce_parts(part, 1, blocks, a.head_dim, dgain_q, dgain_k, a.dtype, stream);
+  return launch_reduce_parts(part, 1, g.blocks, a.head_dim, dgain_q, dgain_k, a.dtype, stream);
 }
 
 }  // namespace pf
