@@ -123,7 +123,7 @@ cudaError_t launch_layernorm_bwd(const LnArgs& a, void* dweight, void* dbias, fl
 // Pairs of a head vector: elements, axis (n_axes: not rotated) and turns per unit position.
 struct RopeTable {
   double turns[128];
-  uint8_t e0[128], e1[128], axis[128];
+  alignas(4) uint8_t e0[128], e1[128], axis[128];  // read four at a time
   int half_align;  // greatest power of two (at most 4) dividing every section's half width
 };
 struct RopeArgs {

@@ -11,13 +11,14 @@
 // A lane owns four pairs of a vector, so a pair's elements meet in one lane's registers for
 // either pairing: one 16-byte access for interleaved pairs (e1 = e0 + 1), two 8-byte ones for
 // half-split pairs (e1 = e0 + w_a / 2).  A block takes 1 to 8 tokens; its threads first compute the
-// tokens' cosines and sines once, into shared memory (behind the first loads), then each warp
-// walks its share of a token's heads, 32 / SEG vectors at a time with kUnroll steps of loads in
-// flight.  Angles are taken in turns, pos * (theta^(-2i/w) / 2 pi) in 64 bits, and only their
+// tokens' cosines and sines once, into shared memory, then each warp walks its share of a
+// token's heads, 32 / SEG vectors a step, several steps' loads in flight.  Angles are taken in turns, pos * (theta^(-2i/w) / 2 pi) in 64 bits, and only their
 // fraction is rounded to 32 bits, so far positions lose nothing.
 //
 // The backward pass keeps the gain-gradient sums of a lane's elements in registers while its
 // block walks tokens; blocks write fp32 partials that a second kernel adds in a fixed order.
+
+#include <type_traits>
 
 #include "block_ops.cuh"
 
@@ -28,8 +29,8 @@ using namespace blk;
 
 constexpr int kWarps = 8;
 
-struct RopeParams {
-  const void* x[2];   // q, k: forward input, backward saved input (null without norm)
+struct RopeParams {  // (pointers and strides of q, k)
+  const void* x[2];   // forward input, backward saved input (null without norm)
   const void* dy[2];  // backward: gradients of the rotated output
   void* y[2];         // forward: output; backward: dx
   const void* gain[2];
@@ -77,39 +78,64 @@ struct Raw {
       }
     }
   }
-  // first and second elements of the four pairs
-  __device__ __forceinline__ void get(float (&a)[4], float (&b)[4]) const {
+  __device__ __forceinline__ T first(int k) const { return INTER ? v[0].v[2 * k] : v[k / PV].v[k % PV]; }
+  __device__ __forceinline__ T second(int k) const {
+    return INTER ? v[0].v[2 * k + 1] : v[4 / PV + k / PV].v[k % PV];
+  }
+  // first (a) and second (b) elements of pairs 0, 1 and 2, 3
+  __device__ __forceinline__ void get(float2 (&a)[2], float2 (&b)[2]) const {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      a[k] = to_f<T>(INTER ? v[0].v[2 * k] : v[k / PV].v[k % PV]);
-      b[k] = to_f<T>(INTER ? v[0].v[2 * k + 1] : v[4 / PV + k / PV].v[k % PV]);
+    for (int j = 0; j < 2; ++j) {
+      a[j] = make_float2(to_f<T>(first(2 * j)), to_f<T>(first(2 * j + 1)));
+      b[j] = make_float2(to_f<T>(second(2 * j)), to_f<T>(second(2 * j + 1)));
     }
   }
-  __device__ __forceinline__ void put(const float (&a)[4], const float (&b)[4]) {
+  __device__ __forceinline__ void put(const float2 (&a)[2], const float2 (&b)[2]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      (INTER ? v[0].v[2 * k] : v[k / PV].v[k % PV]) = from_f<T>(a[k]);
-      (INTER ? v[0].v[2 * k + 1] : v[4 / PV + k / PV].v[k % PV]) = from_f<T>(b[k]);
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (INTER) {
+        put2(v[0].v + 4 * j, a[j].x, b[j].x);
+        put2(v[0].v + 4 * j + 2, a[j].y, b[j].y);
+      } else if constexpr (PV >= 2) {
+        put2(v[2 * j / PV].v + 2 * j % PV, a[j].x, a[j].y);
+        put2(v[4 / PV + 2 * j / PV].v + 2 * j % PV, b[j].x, b[j].y);
+      } else {
+        v[2 * j].v[0] = from_f<T>(a[j].x);
+        v[2 * j + 1].v[0] = from_f<T>(a[j].y);
+        v[4 + 2 * j].v[0] = from_f<T>(b[j].x);
+        v[5 + 2 * j].v[0] = from_f<T>(b[j].y);
+      }
+    }
+  }
+  static __device__ __forceinline__ void put2(T* to, float x, float y) {
+    if constexpr (sizeof(T) == 4) {
+      to[0] = x;
+      to[1] = y;
+    } else if constexpr (std::is_same<T, __half>::value) {
+      *reinterpret_cast<__half2*>(to) = __floats2half2_rn(x, y);
+    } else {
+      *reinterpret_cast<__nv_bfloat162*>(to) = __floats2bfloat162_rn(x, y);
     }
   }
 };
 
-// cos and sin of every pair of the block's tokens, [token of the block][pair].
-__device__ __forceinline__ void fill_angles(const RopeParams& p, float2* cs, unsigned first, int count) {
-  const int pairs = p.head_dim / 2;
-  for (int i = threadIdx.x; i < count * pairs; i += 32 * kWarps) {
-    const int t = i / pairs, k = i - t * pairs;
-    const unsigned bt = first + t;
-    if (bt >= static_cast<unsigned>(p.total)) break;
-    const unsigned b = bt / static_cast<unsigned>(p.tokens), tok = bt - b * static_cast<unsigned>(p.tokens);
-    const int axis = p.tab.axis[k];
-    float c = 1.f, s = 0.f;
-    if (axis < p.n_axes) {
-      const float at = __ldg(p.pos + b * p.pos_batch + static_cast<long long>(tok) * p.n_axes + axis);
-      const double turns = static_cast<double>(at) * p.tab.turns[k];
-      sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
-    }
-    cs[t * 128 + k] = make_float2(c, s);
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+// a where the bits of pairs 2 j and 2 j + 1 are set, else b
+__device__ __forceinline__ float2 pick(unsigned bits, int j, float2 a, float2 b) {
+  return make_float2(bits >> (2 * j) & 1u ? a.x : b.x, bits >> (2 * j + 1) & 1u ? a.y : b.y);
+}
+
+// cos and sin of a lane's four pairs.
+__device__ __forceinline__ void read_angles(const float2* at, float2 (&c)[2], float2 (&s)[2]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float2 u = at[2 * j], v = at[2 * j + 1];
+    c[j] = make_float2(u.x, v.x);
+    s[j] = make_float2(u.y, v.y);
   }
 }
 
@@ -120,244 +146,254 @@ __device__ __forceinline__ float seg_sum(float v) {
   return v;
 }
 
-// This warp's token and heads of a block's tokens.
-struct Item {
-  unsigned b, tok;
-  int slot, lo, hi;  // token of the block; heads [lo, hi) of q's and k's together
-  bool on;
-  __device__ Item(const RopeParams& p, unsigned first, int warp, int split, int splits) {
-    slot = warp / p.shares;
-    const unsigned bt = first + slot;
-    on = bt < static_cast<unsigned>(p.total);
-    b = bt / static_cast<unsigned>(p.tokens);
-    tok = bt - b * static_cast<unsigned>(p.tokens);
-    const int n = p.heads[0] + p.heads[1], share = split * p.shares + warp % p.shares, all = splits * p.shares;
-    lo = static_cast<int>(static_cast<long long>(n) * share / all);
-    hi = static_cast<int>(static_cast<long long>(n) * (share + 1) / all);
-  }
-};
-
-// A lane's place in a vector.
+// A lane's place in a vector: its pairs' elements (three table words, four pairs each).
 struct Lane {
   int sub, e0[4], e1[4], pair0;
   bool active;
   unsigned turn;  // bit k: pair k turns (pairs past the axes are copied)
-  template <int SEG>
+  template <bool INTER, int SEG>
   static __device__ __forceinline__ Lane make(const RopeParams& p) {
     Lane l;
     const int lane = threadIdx.x & 31, chunk = lane % SEG;
     l.sub = lane / SEG;
     l.active = chunk * 8 < p.head_dim;
     l.pair0 = l.active ? chunk * 4 : 0;
+    const uint32_t ax = *reinterpret_cast<const uint32_t*>(p.tab.axis + l.pair0);
+    const uint32_t w0 = INTER ? 0u : *reinterpret_cast<const uint32_t*>(p.tab.e0 + l.pair0);
+    const uint32_t w1 = INTER ? 0u : *reinterpret_cast<const uint32_t*>(p.tab.e1 + l.pair0);
     l.turn = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      l.e0[k] = p.tab.e0[l.pair0 + k];
-      l.e1[k] = p.tab.e1[l.pair0 + k];
-      l.turn |= (p.tab.axis[l.pair0 + k] < p.n_axes ? 1u : 0u) << k;
+      l.e0[k] = INTER ? 2 * (l.pair0 + k) : static_cast<int>(w0 >> (8 * k) & 255u);
+      l.e1[k] = INTER ? 2 * (l.pair0 + k) + 1 : static_cast<int>(w1 >> (8 * k) & 255u);
+      l.turn |= (static_cast<int>(ax >> (8 * k) & 255u) < p.n_axes ? 1u : 0u) << k;
     }
     return l;
   }
 };
 
-template <typename T, bool INTER, int PV, int SEG>
+// This warp's token and its share of the token's heads.
+struct Item {
+  unsigned b, tok;
+  int slot, share;   // token of the block, share of the token within the block
+  int lo[2], hi[2];  // heads of q, k
+  bool on;
+  __device__ Item(const RopeParams& p, unsigned first, int warp, int split, int splits) {
+    slot = warp / p.shares;
+    share = warp - slot * p.shares;
+    const unsigned bt = first + slot;
+    on = bt < static_cast<unsigned>(p.total);
+    b = bt / static_cast<unsigned>(p.tokens);
+    tok = bt - b * static_cast<unsigned>(p.tokens);
+    const int n = p.heads[0] + p.heads[1], at = split * p.shares + share, all = splits * p.shares;
+    const int each = n / all, more = n - each * all;  // the first `more` shares take one head more
+    const int from = at * each + min(at, more), to = on ? from + each + (at < more ? 1 : 0) : from;
+    lo[0] = min(from, p.heads[0]);
+    hi[0] = min(to, p.heads[0]);
+    lo[1] = max(from - p.heads[0], 0);
+    hi[1] = max(to - p.heads[0], 0);
+  }
+  // cos and sin of the token's pairs into `cs`, by the warps that share the token
+  __device__ __forceinline__ void fill_angles(const RopeParams& p, float2* cs) const {
+    if (!on) return;
+    for (int k = (threadIdx.x & 31) + 32 * share; k < p.head_dim / 2; k += 32 * p.shares) {
+      const int axis = p.tab.axis[k];
+      float c = 1.f, s = 0.f;
+      if (axis < p.n_axes) {
+        const float at = __ldg(p.pos + b * p.pos_batch + static_cast<long long>(tok) * p.n_axes + axis);
+        const double turns = static_cast<double>(at) * p.tab.turns[k];
+        sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
+      }
+      cs[slot * 128 + k] = make_float2(c, s);
+    }
+  }
+  // this lane's first vector of operand w of a tensor, and the distance between its vectors
+  template <typename T, int PER>
+  __device__ __forceinline__ T* start(const void* base, const long long (&st)[3], int w, const Lane& ln, long long& step) const {
+    step = st[2] * PER;
+    return static_cast<T*>(const_cast<void*>(base)) + b * st[0] + tok * st[1] + (lo[w] + ln.sub) * st[2];
+  }
+};
+
+template <typename T, bool INTER, int PV>
+__device__ __forceinline__ void load_gain(const void* g, const Lane& ln, float2 (&ga)[2], float2 (&gb)[2]) {
+  ga[0] = ga[1] = gb[0] = gb[1] = both(1.f);
+  if (g != nullptr) {
+    Raw<T, INTER, PV> r;
+    r.load(static_cast<const T*>(g), ln.e0, ln.e1);
+    r.get(ga, gb);
+  }
+}
+
+// FULL: every pair turns.
+template <typename T, bool INTER, int PV, int SEG, bool FULL>
 __global__ void __launch_bounds__(32 * kWarps) rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPer = 32 / SEG;
-  constexpr int kUnroll = 4;
+  constexpr int kSteps = 4;
   __shared__ float2 cs[kWarps * 128];
-  const Lane ln = Lane::make<SEG>(p);
-  const int per_block = kWarps / p.shares;
-  const unsigned first = blockIdx.x * static_cast<unsigned>(per_block);
-  const Item it(p, first, threadIdx.x >> 5, blockIdx.y, gridDim.y);
+  const Lane ln = Lane::make<INTER, SEG>(p);
+  const Item it(p, blockIdx.x * static_cast<unsigned>(kWarps / p.shares), threadIdx.x >> 5, blockIdx.y, gridDim.y);
   const float inv_d = 1.f / static_cast<float>(p.head_dim);
   const bool norm = p.eps > 0.f;
-  bool filled = false;
-  float c[4], s[4];
+  it.fill_angles(p, cs);
+  __syncthreads();
+  float2 c[2], s[2];
+  read_angles(cs + it.slot * 128 + ln.pair0, c, s);
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const int lo = w ? max(it.lo - p.heads[0], 0) : it.lo, hi = w ? it.hi - p.heads[0] : min(it.hi, p.heads[0]);
-    if (w == 1 && (!it.on || lo >= hi)) break;
-    const bool any = it.on && lo < hi;
-    const T* x = static_cast<const T*>(p.x[w]) + it.b * p.xs[w][0] + it.tok * p.xs[w][1];
-    T* y = static_cast<T*>(p.y[w]) + it.b * p.ys[w][0] + it.tok * p.ys[w][1];
-    float ga[4], gb[4];
+    if (it.lo[w] >= it.hi[w]) continue;
+    float2 ga[2], gb[2];
+    load_gain<T, INTER, PV>(p.gain[w], ln, ga, gb);
+    long long xstep, ystep;
+    const T* x = it.start<T, kPer>(p.x[w], p.xs[w], w, ln, xstep);
+    T* y = it.start<T, kPer>(p.y[w], p.ys[w], w, ln, ystep);
+    // vectors of this lane left (none for a lane past the vector's end)
+    int left = ln.active ? it.hi[w] - it.lo[w] - ln.sub : 0;
+    for (int steps = (it.hi[w] - it.lo[w] + kPer - 1) / kPer; steps > 0; steps -= kSteps) {
+      Raw<T, INTER, PV> raw[kSteps];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) ga[k] = gb[k] = 1.f;
-    if (any && p.gain[w] != nullptr) {
-      Raw<T, INTER, PV> g;
-      g.load(static_cast<const T*>(p.gain[w]), ln.e0, ln.e1);
-      g.get(ga, gb);
-    }
-    for (int h0 = lo; h0 < hi || !filled; h0 += kPer * kUnroll) {
-      Raw<T, INTER, PV> raw[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = h0 + u * kPer + ln.sub;
-        if (any && ln.active && h < hi)
-          raw[u].load(x + h * p.xs[w][2], ln.e0, ln.e1);
-        else
-          raw[u].zero();
+      for (int u = 0; u < kSteps; ++u) {
+        raw[u].zero();
+        if (u * kPer < left) raw[u].load(x, ln.e0, ln.e1);
+        x += xstep;
       }
-      if (!filled) {
-        fill_angles(p, cs, first, per_block);
-        __syncthreads();
-        filled = true;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 v = cs[it.slot * 128 + ln.pair0 + k];
-          c[k] = v.x;
-          s[k] = v.y;
+      for (int u = 0; u < kSteps; ++u) {
+        if (u >= steps) break;  // the whole warp
+        float2 a[2], b[2], ya[2], yb[2];
+        raw[u].get(a, b);
+        float2 r = both(1.f);
+        if (norm) {
+          const float2 q = fma2(a[0], a[0], fma2(b[0], b[0], fma2(a[1], a[1], mul2(b[1], b[1]))));
+          r = both(rsqrtf(fmaf(seg_sum<SEG>(q.x + q.y), inv_d, p.eps)));
         }
-      }
-      float a[kUnroll][4], b[kUnroll][4], r[kUnroll];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        raw[u].get(a[u], b[u]);
-        r[u] = 1.f;
-      }
-      if (norm) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          float ss = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ss = fmaf(a[u][k], a[u][k], fmaf(b[u][k], b[u][k], ss));
-          r[u] = rsqrtf(fmaf(seg_sum<SEG>(ss), inv_d, p.eps));
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = h0 + u * kPer + ln.sub;
-        float ya[4], yb[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float za = a[u][k] * (r[u] * ga[k]), zb = b[u][k] * (r[u] * gb[k]);
-          const bool turn = ln.turn >> k & 1u;
-          ya[k] = turn ? za * c[k] - zb * s[k] : za;
-          yb[k] = turn ? za * s[k] + zb * c[k] : zb;
+        for (int j = 0; j < 2; ++j) {
+          a[j] = mul2(a[j], mul2(r, ga[j]));
+          b[j] = mul2(b[j], mul2(r, gb[j]));
+          ya[j] = fma2(a[j], c[j], mul2(b[j], neg(s[j])));
+          yb[j] = fma2(a[j], s[j], mul2(b[j], c[j]));
+          if (!FULL) {
+            ya[j] = pick(ln.turn, j, ya[j], a[j]);
+            yb[j] = pick(ln.turn, j, yb[j], b[j]);
+          }
         }
         raw[u].put(ya, yb);
-        if (any && ln.active && h < hi) raw[u].store(y + h * p.ys[w][2], ln.e0, ln.e1);
+        if (u * kPer < left) raw[u].store(y, ln.e0, ln.e1);
+        y += ystep;
       }
+      left -= kPer * kSteps;
     }
   }
 }
 
-template <typename T, bool INTER, int PV, int SEG>
+template <typename T, bool INTER, int PV, int SEG, bool FULL>
 __global__ void __launch_bounds__(32 * kWarps, 2) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPer = 32 / SEG;
-  constexpr int kUnroll = 2;
+  constexpr int kSteps = 2;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ float2 cs[2][kWarps * 128];
   __shared__ float red[2][256];
-  const Lane ln = Lane::make<SEG>(p);
+  const Lane ln = Lane::make<INTER, SEG>(p);
   const int warp = threadIdx.x >> 5;
-  const int per_block = kWarps / p.shares;
-  float sa[2][4], sb[2][4];
+  float2 sa[2][2], sb[2][2];  // gain gradients of q, k
 #pragma unroll
   for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sa[w][k] = sb[w][k] = 0.f;
+    for (int j = 0; j < 2; ++j) sa[w][j] = sb[w][j] = both(0.f);
   const float inv_d = 1.f / static_cast<float>(p.head_dim);
   const bool norm = p.eps > 0.f;
-  const unsigned stride = gridDim.x * static_cast<unsigned>(per_block);
+  const unsigned per_block = static_cast<unsigned>(kWarps / p.shares), stride = gridDim.x * per_block;
   int buf = 0;
-  for (unsigned first = blockIdx.x * static_cast<unsigned>(per_block); first < static_cast<unsigned>(p.total);
-       first += stride, buf ^= 1) {
+  for (unsigned first = blockIdx.x * per_block; first < static_cast<unsigned>(p.total); first += stride, buf ^= 1) {
     const Item it(p, first, warp, 0, 1);
-    bool filled = false;
-    float c[4], s[4];
+    // two tables in turn: the barrier of the next tokens also covers this one's readers
+    it.fill_angles(p, cs[buf]);
+    __syncthreads();
+    float2 c[2], s[2];
+    read_angles(cs[buf] + it.slot * 128 + ln.pair0, c, s);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const int lo = w ? max(it.lo - p.heads[0], 0) : it.lo, hi = w ? it.hi - p.heads[0] : min(it.hi, p.heads[0]);
-      if (w == 1 && (!it.on || lo >= hi)) break;
-      const bool any = it.on && lo < hi;
-      const T* x = static_cast<const T*>(p.x[w]) + it.b * p.xs[w][0] + it.tok * p.xs[w][1];
-      const T* d = static_cast<const T*>(p.dy[w]) + it.b * p.ds[w][0] + it.tok * p.ds[w][1];
-      T* y = static_cast<T*>(p.y[w]) + it.b * p.ys[w][0] + it.tok * p.ys[w][1];
-      float ga[4], gb[4];
+      if (it.lo[w] >= it.hi[w]) continue;
+      float2 ga[2], gb[2];
+      load_gain<T, INTER, PV>(p.gain[w], ln, ga, gb);
+      long long xstep = 0, dstep, ystep;
+      const T* x = norm ? it.start<T, kPer>(p.x[w], p.xs[w], w, ln, xstep) : nullptr;
+      const T* d = it.start<T, kPer>(p.dy[w], p.ds[w], w, ln, dstep);
+      T* y = it.start<T, kPer>(p.y[w], p.ys[w], w, ln, ystep);
+      int left = ln.active ? it.hi[w] - it.lo[w] - ln.sub : 0;
+      for (int steps = (it.hi[w] - it.lo[w] + kPer - 1) / kPer; steps > 0; steps -= kSteps) {
+        Raw<T, INTER, PV> rd[kSteps], rx[kSteps];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) ga[k] = gb[k] = 1.f;
-      if (any && p.gain[w] != nullptr) {
-        Raw<T, INTER, PV> g;
-        g.load(static_cast<const T*>(p.gain[w]), ln.e0, ln.e1);
-        g.get(ga, gb);
-      }
-      for (int h0 = lo; h0 < hi || !filled; h0 += kPer * kUnroll) {
-        Raw<T, INTER, PV> rd[kUnroll], rx[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int h = h0 + u * kPer + ln.sub;
+        for (int u = 0; u < kSteps; ++u) {
           rd[u].zero();
           rx[u].zero();
-          if (any && ln.active && h < hi) {
-            rd[u].load(d + h * p.ds[w][2], ln.e0, ln.e1);
-            if (norm) rx[u].load(x + h * p.xs[w][2], ln.e0, ln.e1);
+          if (u * kPer < left) {
+            rd[u].load(d, ln.e0, ln.e1);
+            if (norm) rx[u].load(x, ln.e0, ln.e1);
           }
-        }
-        if (!filled) {
-          // two tables in turn: the barrier of the next tokens also covers this one's readers
-          fill_angles(p, cs[buf], first, per_block);
-          __syncthreads();
-          filled = true;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 v = cs[buf][it.slot * 128 + ln.pair0 + k];
-            c[k] = v.x;
-            s[k] = v.y;
-          }
+          d += dstep;
+          x += xstep;
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int h = h0 + u * kPer + ln.sub;
-          float da[4], db[4], za[4], zb[4];
+        for (int u = 0; u < kSteps; ++u) {
+          if (u >= steps) break;  // the whole warp
+          float2 da[2], db[2], za[2], zb[2];
           rd[u].get(da, db);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const bool turn = ln.turn >> k & 1u;
-            za[k] = turn ? da[k] * c[k] + db[k] * s[k] : da[k];
-            zb[k] = turn ? db[k] * c[k] - da[k] * s[k] : db[k];
+          for (int j = 0; j < 2; ++j) {
+            za[j] = fma2(da[j], c[j], mul2(db[j], s[j]));
+            zb[j] = fma2(db[j], c[j], mul2(da[j], neg(s[j])));
+            if (!FULL) {
+              za[j] = pick(ln.turn, j, za[j], da[j]);
+              zb[j] = pick(ln.turn, j, zb[j], db[j]);
+            }
           }
           if (norm) {
-            float a[4], b[4], ta[4], tb[4], ss = 0.f, sx = 0.f;
+            float2 a[2], b[2], ta[2], tb[2];
             rx[u].get(a, b);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              ta[k] = za[k] * ga[k];
-              tb[k] = zb[k] * gb[k];
-              ss = fmaf(a[k], a[k], fmaf(b[k], b[k], ss));
-              sx = fmaf(ta[k], a[k], fmaf(tb[k], b[k], sx));
+            for (int j = 0; j < 2; ++j) {
+              ta[j] = mul2(za[j], ga[j]);
+              tb[j] = mul2(zb[j], gb[j]);
             }
-            ss = seg_sum<SEG>(ss);
-            sx = seg_sum<SEG>(sx);
+            const float2 qs = fma2(a[0], a[0], fma2(b[0], b[0], fma2(a[1], a[1], mul2(b[1], b[1]))));
+            const float2 qx = fma2(ta[0], a[0], fma2(tb[0], b[0], fma2(ta[1], a[1], mul2(tb[1], b[1]))));
+            const float ss = seg_sum<SEG>(qs.x + qs.y), sx = seg_sum<SEG>(qx.x + qx.y);
             const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-            const float m = r * r * sx * inv_d;  // r mean(a x^) = r^2 mean(a x): times x, then r
+            const float2 r2 = both(r), m = both(-r * r * sx * inv_d);  // r mean(a x^) = r^2 mean(a x): times x, then r
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int j = 0; j < 2; ++j) {
               // an absent head has dz = x = 0 and adds nothing
-              sa[w][k] = fmaf(za[k], a[k] * r, sa[w][k]);
-              sb[w][k] = fmaf(zb[k], b[k] * r, sb[w][k]);
-              za[k] = r * (ta[k] - a[k] * m);
-              zb[k] = r * (tb[k] - b[k] * m);
+              sa[w][j] = fma2(za[j], mul2(a[j], r2), sa[w][j]);
+              sb[w][j] = fma2(zb[j], mul2(b[j], r2), sb[w][j]);
+              za[j] = mul2(r2, fma2(a[j], m, ta[j]));
+              zb[j] = mul2(r2, fma2(b[j], m, tb[j]));
             }
           }
-          if (any && ln.active && h < hi) {
+          if (u * kPer < left) {
             rd[u].put(za, zb);
-            rd[u].store(y + h * p.ys[w][2], ln.e0, ln.e1);
+            rd[u].store(y, ln.e0, ln.e1);
           }
+          y += ystep;
         }
+        left -= kPer * kSteps;
       }
     }
   }
   if (p.part == nullptr) return;
   // the warp's sub-vectors, then the block's warps in order
+  float v[2][2][4];  // [q, k][first, second][pair]
 #pragma unroll
   for (int w = 0; w < 2; ++w)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
+      v[w][0][k] = k & 1 ? sa[w][k / 2].y : sa[w][k / 2].x;
+      v[w][1][k] = k & 1 ? sb[w][k / 2].y : sb[w][k / 2].x;
 #pragma unroll
       for (int off = 16; off >= SEG; off >>= 1) {
-        sa[w][k] += __shfl_xor_sync(0xffffffffu, sa[w][k], off);
-        sb[w][k] += __shfl_xor_sync(0xffffffffu, sb[w][k], off);
+        v[w][0][k] += __shfl_xor_sync(0xffffffffu, v[w][0][k], off);
+        v[w][1][k] += __shfl_xor_sync(0xffffffffu, v[w][1][k], off);
       }
     }
   for (int wi = 0; wi < kWarps; ++wi) {
@@ -366,8 +402,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rope_bwd_kernel(const __grid_c
       for (int w = 0; w < 2; ++w)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          red[w][ln.e0[k]] = wi == 0 ? sa[w][k] : red[w][ln.e0[k]] + sa[w][k];
-          red[w][ln.e1[k]] = wi == 0 ? sb[w][k] : red[w][ln.e1[k]] + sb[w][k];
+          red[w][ln.e0[k]] = wi == 0 ? v[w][0][k] : red[w][ln.e0[k]] + v[w][0][k];
+          red[w][ln.e1[k]] = wi == 0 ? v[w][1][k] : red[w][ln.e1[k]] + v[w][1][k];
         }
     }
     __syncthreads();
@@ -377,13 +413,20 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rope_bwd_kernel(const __grid_c
     out[e] = red[e >= p.head_dim][e >= p.head_dim ? e - p.head_dim : e];
 }
 
+template <typename T, bool INTER, int PV, int SEG, bool FULL>
+cudaError_t launch_full(const RopeParams& p, bool bwd, dim3 blocks, cudaStream_t stream) {
+  if (bwd)
+    rope_bwd_kernel<T, INTER, PV, SEG, FULL><<<blocks, 32 * kWarps, 0, stream>>>(p);
+  else
+    rope_fwd_kernel<T, INTER, PV, SEG, FULL><<<blocks, 32 * kWarps, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <typename T, bool INTER, int PV, int SEG>
 cudaError_t launch_kernel(const RopeParams& p, bool bwd, dim3 blocks, cudaStream_t stream) {
-  if (bwd)
-    rope_bwd_kernel<T, INTER, PV, SEG><<<blocks, 32 * kWarps, 0, stream>>>(p);
-  else
-    rope_fwd_kernel<T, INTER, PV, SEG><<<blocks, 32 * kWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+  // the last pair turns: all do, as the sections come first
+  if (p.tab.axis[p.head_dim / 2 - 1] < p.n_axes) return launch_full<T, INTER, PV, SEG, true>(p, bwd, blocks, stream);
+  return launch_full<T, INTER, PV, SEG, false>(p, bwd, blocks, stream);
 }
 
 template <typename T, bool INTER, int PV>
