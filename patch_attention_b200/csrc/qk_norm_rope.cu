@@ -10,7 +10,7 @@
 // HBM bound: every element is read once and written once (backward: two reads, one write).
 // A lane owns four pairs of a vector, so a pair's elements meet in one lane's registers for
 // either pairing: one 16-byte access for interleaved pairs (e1 = e0 + 1), two 8-byte ones for
-// half-split pairs (e1 = e0 + w_a / 2).  A block takes 1 to 8 tokens; its threads first compute the
+// half-split pairs (e1 = e0 + w_a / 2).  A block takes 1 to 4 tokens; its threads first compute the
 // tokens' cosines and sines once, into shared memory, then each warp walks its share of a
 // token's heads, 32 / SEG vectors a step, several steps' loads in flight.  Angles are taken in turns, pos * (theta^(-2i/w) / 2 pi) in 64 bits, and only their
 // fraction is rounded to 32 bits, so far positions lose nothing.
@@ -27,7 +27,7 @@ namespace {
 
 using namespace blk;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 struct RopeParams {  // (pointers and strides of q, k)
   const void* x[2];   // forward input, backward saved input (null without norm)
@@ -40,7 +40,7 @@ struct RopeParams {  // (pointers and strides of q, k)
   float* part;        // backward: [block][2][head_dim], or null
   int total;          // batch * tokens
   int tokens, n_axes, heads[2], head_dim;
-  int shares;         // warps of a block that share a token's heads: 1, 2, 4 or 8
+  int shares;         // warps of a block that share a token's heads: 1, 2 or 4
   float eps;          // 0: no norm
   RopeTable tab;
 };
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(32 * kWarps) rope_fwd_kernel(const __grid_cons
 }
 
 template <typename T, bool INTER, int PV, int SEG, bool FULL>
-__global__ void __launch_bounds__(32 * kWarps, 2) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 4) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPer = 32 / SEG;
   constexpr int kSteps = 2;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -457,7 +457,8 @@ cudaError_t dispatch(const RopeArgs& a, const RopeParams& p, bool bwd, dim3 bloc
 }
 
 // How a call's tokens and heads are laid over blocks: `shares` warps per token so that the
-// tokens give every SM sixteen warps or more, and, where eight are not enough, the heads of a
+// tokens give every SM 64 warps (several rounds of what is resident: a short last round costs
+// little), and, where kWarps are not enough, the heads of a
 // token over `splits` blocks (forward only).
 struct Grid {
   int shares, splits, blocks;
@@ -466,17 +467,18 @@ Grid grid_of(const RopeParams& p, bool bwd) {
   const int chunks = p.head_dim / 8;
   const int per_step = chunks <= 4 ? 8 : chunks <= 8 ? 4 : chunks <= 16 ? 2 : 1;  // vectors of a warp at once
   const long long steps = (p.heads[0] + p.heads[1] + per_step - 1) / per_step;    // most warps with work
-  const long long want = (148 * 16 + p.total - 1) / p.total;
+  const long long want = (148 * 64 + p.total - 1) / p.total;
   Grid g = {1, 1, 0};
-  while (g.shares < 8 && g.shares < want && g.shares < steps) g.shares *= 2;
-  if (!bwd && g.shares == 8) {
+  while (g.shares < kWarps && g.shares < want && g.shares < steps) g.shares *= 2;
+  if (!bwd && g.shares == kWarps) {
     const long long more = want < steps ? want : steps;
-    g.splits = static_cast<int>((more + 7) / 8);
+    g.splits = static_cast<int>((more + kWarps - 1) / kWarps);
   }
   const int per_block = kWarps / g.shares;
   g.blocks = (p.total + per_block - 1) / per_block;
-  // backward: two blocks per SM walk the tokens, so that few partial gain gradients are written
-  if (bwd && g.blocks > 148 * 2) g.blocks = 148 * 2;
+  // backward: the blocks that are resident at once walk the tokens, so that few partial gain
+  // gradients are written
+  if (bwd && g.blocks > 148 * 4) g.blocks = 148 * 4;
   return g;
 }
 
