@@ -200,11 +200,21 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
   }
   if (mk.doc_q != nullptr) {
     const int* ids = mk.doc_k + static_cast<long long>(w.b) * mk.n_k;
-    for (int j = w.j0 + warp; j < w.j1; j += kThreads / 32) {
-      const DocRange r = doc_range(ids, j * kRows, min(kRows, mk.n_k - j * kRows), lane);
-      int c = doc_class(qdoc[0], r);
-      if (NQ == 2) c |= doc_class(qdoc[NQ - 1], r) << 2;
-      if (lane == 0) cls[j - w.j0] = static_cast<uint8_t>(c);
+    constexpr int kWarps = kThreads / 32, kAtOnce = 4;
+    for (int j = w.j0 + warp; j < w.j1; j += kWarps * kAtOnce) {
+      DocIds d[kAtOnce];
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int jx = j + x * kWarps;
+        d[x].load(ids, jx * kRows, jx < w.j1 ? mk.n_k - jx * kRows : 0, lane);
+      }
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const DocRange r = d[x].range();
+        int c = doc_class(qdoc[0], r);
+        if (NQ == 2) c |= doc_class(qdoc[NQ - 1], r) << 2;
+        if (lane == 0 && j + x * kWarps < w.j1) cls[j + x * kWarps - w.j0] = static_cast<uint8_t>(c);
+      }
     }
   }
   tc_fence_before();
@@ -410,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
     const int doc = in_range && mk.doc_q != nullptr ? __ldg(mk.doc_q + static_cast<long long>(w.b) * mk.n_q + query) : -1;
     const int* ids = mk.doc_k + static_cast<long long>(w.b) * mk.n_k;
     const float slope = MOD && mk.slopes != nullptr && in_range ? __ldg(mk.slopes + head) * kLog2e : 0.f;
-    const float place = static_cast<float>(query + (mk.n_k - mk.n_q));
+    const int place = query + (mk.n_k - mk.n_q);
     const float c = MOD ? 1.f : mk.scale_log2;
     float m = -INFINITY;  // reference row maximum, in log2 units
     float l = 0.f;
@@ -436,20 +446,11 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
         tmem_ld32(tS + h * 64 + 32, s + 32);
         tmem_wait_ld();
         reg_fence<64>(s);
+        float rest = 0.f;  // to be added to every score of the row
         if constexpr (MOD) {
-          if (mk.cap_log2 > 0.f) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k) s[k] = __float_as_uint(cap_score(__uint_as_float(s[k]), mk));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 64; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * mk.scale_log2);
-          }
-          if (mk.slopes != nullptr) {
-            const float d0 = place - static_cast<float>(base);
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-              s[k] = __float_as_uint(fmaf(-slope, fabsf(d0 - static_cast<float>(k)), __uint_as_float(s[k])));
-          }
+          if (mk.cap_log2 > 0.f) tanh_scores<64>(s, mk);
+          scale_scores<64>(s, mk.cap_log2 > 0.f ? mk.cap_log2 : mk.scale_log2);
+          if (mk.slopes != nullptr) rest = add_bias<64>(s, slope, base - place);
         }
         if (kind == 1) {
           uint64_t bits = limit_bits(limit, base);
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
             if (!(hi >> k & 1u)) s[k + 32] = __float_as_uint(-INFINITY);
           }
         }
-        const float mxs = row_max64(s) * c;
+        const float mxs = MOD ? row_max64(s) + rest : row_max64(s) * c;
         // O is rescaled only when the maximum grows by more than 2^8 (or is NaN): exact, as the
         // final O / l uses one reference for both
         const bool grow = in_range && !(mxs <= m + 8.f);
@@ -494,12 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
         const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: every p is 0
         uint32_t pk[32];
         {
-          const float2 cc = make_float2(c, c), nm = make_float2(-ref, -ref);
+          const float2 cc = both(c), nm = both(rest - ref);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                            make_float2(0.f, 0.f)};
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), cc, nm);
+            const float2 raw = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+            const float2 x = MOD ? __fadd2_rn(raw, nm) : __ffma2_rn(raw, cc, nm);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
             acc[k & 3] = __fadd2_rn(acc[k & 3], e);
             pk[k] = pack2(e.x, e.y);  // bf16 probabilities: the MMA's operand type

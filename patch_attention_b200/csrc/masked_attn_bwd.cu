@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sX = smem;                       // X1, X2
   uint8_t* sY = smem + 2 * Dm::kTileBytes;  // [stage] Y1, Y2
-  float* stat = reinterpret_cast<float*>(sY + 2 * S * Dm::kTileBytes);  // [stage] lse[128], delta[128]
+  float* stat = reinterpret_cast<float*>(sY + 2 * S * Dm::kTileBytes);  // [stage] -lse[128] (log2), -delta[128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(stat + S * 2 * kRows);
   uint64_t* x_full = bars;
   uint64_t* y_full = bars + 1;
@@ -126,10 +126,21 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
   if (docs) {
     const DocRange mine = doc_range((KEYS ? mk.doc_k + bk : mk.doc_q + bq), x0,
                                     min(kRows, (KEYS ? mk.n_k : mk.n_q) - x0), lane);
-    for (int j = warp; j < y_tiles; j += kThreads / 32) {
-      const DocRange r = doc_range((KEYS ? mk.doc_q + bq : mk.doc_k + bk), j * kRows,
-                                   min(kRows, (KEYS ? mk.n_q : mk.n_k) - j * kRows), lane);
-      if (lane == 0) cls[j] = static_cast<uint8_t>(doc_class(mine, r));
+    const int* ids = KEYS ? mk.doc_q + bq : mk.doc_k + bk;
+    const int count = KEYS ? mk.n_q : mk.n_k;
+    constexpr int kWarps = kThreads / 32, kAtOnce = 4;
+    for (int j = warp; j < y_tiles; j += kWarps * kAtOnce) {
+      DocIds d[kAtOnce];
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int jx = j + x * kWarps;
+        d[x].load(ids, jx * kRows, jx < y_tiles ? count - jx * kRows : 0, lane);
+      }
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const DocRange r = d[x].range();
+        if (lane == 0 && j + x * kWarps < y_tiles) cls[j + x * kWarps] = static_cast<uint8_t>(doc_class(mine, r));
+      }
     }
   }
   tc_fence_before();
@@ -293,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
             const float l = query < mk.n_q ? __ldg(p.lse + row + query) : -INFINITY;
             unseen[x] = l == -INFINITY;
             // a query that sees nothing: exp2(s - inf) = 0
-            out[x * 32 + lane] = unseen[x] ? INFINITY : l * kLog2e;
-            out[kRows + x * 32 + lane] = unseen[x] ? 0.f : __ldg(p.delta + row + query);
+            out[x * 32 + lane] = unseen[x] ? -INFINITY : -l * kLog2e;
+            out[kRows + x * 32 + lane] = unseen[x] ? 0.f : -__ldg(p.delta + row + query);
           }
         } else {
           const bool partly = see(j) == 1;
@@ -357,13 +368,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
     const int* ids = KEYS ? mk.doc_q + bq : mk.doc_k + bk;
     const int y_rows = KEYS ? mk.n_q : mk.n_k;
     const int limit = !KEYS && in_range ? key_limit(mk, row, prefix) : -1;
-    float lse = INFINITY, delta = 0.f;  // queries stay: this row's
+    float neg_lse = -INFINITY, neg_delta = 0.f;  // queries stay: this row's
     if (!KEYS && in_range) {
       const long long at = (static_cast<long long>(b) * p.heads_q + x_head) * mk.n_q + row;
       const float l = __ldg(p.lse + at);
       if (l != -INFINITY) {
-        lse = l * kLog2e;
-        delta = __ldg(p.delta + at);
+        neg_lse = -l * kLog2e;
+        neg_delta = -__ldg(p.delta + at);
       }
     }
     float slope = 0.f;
@@ -373,7 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
       const int st = i % S;
       const int base = j * kRows + h * 64;
       uint64_t bits = ~0ull;
-      if (see(j) == 1) {
+      const bool partly = see(j) == 1;
+      if (partly) {
         if (KEYS) {
           // queries from row - off on see this key; all of them where it lies in the prefix
           if (!in_range)
@@ -399,43 +411,62 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
       if (!ok) break;
       tc_fence_after();
       const float* st_lse = stat + st * 2 * kRows + h * 64;
-      float pd[64];  // p, times 1 - tanh^2 with a cap
+      float2 pd[32];  // p, times 1 - tanh^2 with a cap
 #pragma unroll
       for (int c0 = 0; c0 < 64; c0 += 32) {
         uint32_t s[32], pk[16];
         tmem_ld32(tS + c0, s);
         tmem_wait_ld();
         reg_fence<32>(s);
-        const uint32_t mask = static_cast<uint32_t>(bits >> c0);
+        float rest = 0.f;
+        float2 damp[16];
+        if constexpr (MOD) {
+          if (mk.cap_log2 > 0.f) {
+            tanh_scores<32>(s, mk);
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float e[2];
+            for (int k = 0; k < 16; ++k) {
+              const float2 t = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+              damp[k] = __ffma2_rn(make_float2(-t.x, -t.y), t, both(1.f));
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) damp[k] = both(1.f);
+          }
+          scale_scores<32>(s, mk.cap_log2 > 0.f ? mk.cap_log2 : mk.scale_log2);
+          if (mk.slopes != nullptr) rest = add_bias<32>(s, slope, base + c0 + (KEYS ? off - row : -off - row));
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          float2 ref[2] = {both(neg_lse), both(neg_lse)};
+          if (KEYS) {
+            const float4 l = *reinterpret_cast<const float4*>(st_lse + c0 + 2 * k);
+            ref[0] = make_float2(l.x, l.y);
+            ref[1] = make_float2(l.z, l.w);
+          }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            float x = __uint_as_float(s[k + u]), damp = 1.f;
-            if constexpr (MOD) {
-              if (mk.cap_log2 > 0.f) {
-                const float f = rcp(ex2(x * mk.cap_in) + 1.f);  // tanh = 1 - 2 f, 1 - tanh^2 = 4 f (1 - f)
-                x = fmaf(-2.f * mk.cap_log2, f, mk.cap_log2);
-                damp = 4.f * f * (1.f - f);
-              } else {
-                x *= mk.scale_log2;
-              }
-              if (mk.slopes != nullptr) {
-                const int col = base + c0 + k + u;
-                const int dist = KEYS ? col + off - row : row + off - col;
-                x = fmaf(-slope, fabsf(static_cast<float>(dist)), x);
-              }
-            }
-            const float ref = KEYS ? st_lse[c0 + k + u] : lse;
-            float v = MOD ? ex2(x - ref) : ex2(fmaf(x, mk.scale_log2, -ref));
-            if (!(mask >> (k + u) & 1u)) v = 0.f;
-            e[u] = v;
-            pd[c0 + k + u] = MOD ? v * damp : v;
+            const float2 x = make_float2(__uint_as_float(s[2 * (k + u)]), __uint_as_float(s[2 * (k + u) + 1]));
+            const float2 y = MOD ? __fadd2_rn(__fadd2_rn(x, both(rest)), ref[u]) : __ffma2_rn(x, both(mk.scale_log2), ref[u]);
+            pd[c0 / 2 + k + u] = make_float2(ex2(y.x), ex2(y.y));
           }
-          pk[k / 2] = pack2(e[0], e[1]);
         }
-        if (KEYS) tmem_st16(tS + c0 / 2, pk);
+        if (partly) {
+          const uint32_t mask = static_cast<uint32_t>(bits >> c0);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            if (!(mask >> (2 * k) & 1u)) pd[c0 / 2 + k].x = 0.f;
+            if (!(mask >> (2 * k + 1) & 1u)) pd[c0 / 2 + k].y = 0.f;
+          }
+        }
+        if (KEYS) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) pk[k] = pack2(pd[c0 / 2 + k].x, pd[c0 / 2 + k].y);
+          tmem_st16(tS + c0 / 2, pk);
+        }
+        if constexpr (MOD) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) pd[c0 / 2 + k] = __fmul2_rn(pd[c0 / 2 + k], damp[k]);
+        }
       }
       if (KEYS) {
         tmem_wait_st();
@@ -453,18 +484,31 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
         tmem_ld32(tP + c0, dp);
         tmem_wait_ld();
         reg_fence<32>(dp);
-        const uint32_t mask = static_cast<uint32_t>(bits >> c0);
+        float2 e[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float e[2];
+        for (int k = 0; k < 16; k += 2) {
+          float2 ref[2] = {both(neg_delta), both(neg_delta)};
+          if (KEYS) {
+            const float4 l = *reinterpret_cast<const float4*>(st_lse + kRows + c0 + 2 * k);
+            ref[0] = make_float2(l.x, l.y);
+            ref[1] = make_float2(l.z, l.w);
+          }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float dl = KEYS ? st_lse[kRows + c0 + k + u] : delta;
-            e[u] = pd[c0 + k + u] * (__uint_as_float(dp[k + u]) - dl);
-            if (!(mask >> (k + u) & 1u)) e[u] = 0.f;  // also where a hidden value makes dp NaN
+            const float2 x = make_float2(__uint_as_float(dp[2 * (k + u)]), __uint_as_float(dp[2 * (k + u) + 1]));
+            e[k + u] = __fmul2_rn(pd[c0 / 2 + k + u], __fadd2_rn(x, ref[u]));
           }
-          pk[k / 2] = pack2(e[0], e[1]);
         }
+        if (partly) {  // also where a hidden value makes dp NaN
+          const uint32_t mask = static_cast<uint32_t>(bits >> c0);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            if (!(mask >> (2 * k) & 1u)) e[k].x = 0.f;
+            if (!(mask >> (2 * k + 1) & 1u)) e[k].y = 0.f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) pk[k] = pack2(e[k].x, e[k].y);
         tmem_st16(tP + c0 / 2, pk);
       }
       tmem_wait_st();

@@ -118,29 +118,40 @@ __device__ __forceinline__ uint64_t document_bits(int mine, int id0, int id1) {
   return bits;
 }
 
-// Smallest and largest document of a run of ids (negative ones left out), and whether any
-// id was negative.  Whole-warp; lo > hi: no document.
+// Smallest and largest document of up to 128 ids (negative ones left out), and whether any id was
+// negative.  Whole-warp; lo > hi: no document.  The ids are loaded first, so that several ranges
+// can be in flight.
 struct DocRange {
   int lo, hi;
   bool gaps;
 };
-__device__ __forceinline__ DocRange doc_range(const int* ids, int first, int count, int lane) {
-  int lo = INT32_MAX, hi = -1;
-  bool gaps = false;
-  for (int i = lane; i < count; i += 32) {
-    const int id = __ldg(ids + first + i);
-    if (id < 0) {
-      gaps = true;
-    } else {
-      lo = min(lo, id);
-      hi = max(hi, id);
-    }
+struct DocIds {
+  int id[4];  // -1: no document, INT32_MIN: past the end
+  __device__ __forceinline__ void load(const int* ids, int first, int count, int lane) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      id[x] = x * 32 + lane < count ? max(__ldg(ids + first + x * 32 + lane), -1) : INT32_MIN;
   }
-  DocRange r;
-  r.lo = __reduce_min_sync(0xffffffffu, lo);
-  r.hi = __reduce_max_sync(0xffffffffu, hi);
-  r.gaps = __any_sync(0xffffffffu, gaps);
-  return r;
+  __device__ __forceinline__ DocRange range() const {
+    int lo = INT32_MAX, hi = -1;
+    bool gaps = false;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      gaps = gaps || id[x] == -1;
+      lo = min(lo, id[x] < 0 ? INT32_MAX : id[x]);
+      hi = max(hi, id[x]);
+    }
+    DocRange r;
+    r.lo = __reduce_min_sync(0xffffffffu, lo);
+    r.hi = __reduce_max_sync(0xffffffffu, hi);
+    r.gaps = __any_sync(0xffffffffu, gaps);
+    return r;
+  }
+};
+__device__ __forceinline__ DocRange doc_range(const int* ids, int first, int count, int lane) {
+  DocIds d;
+  d.load(ids, first, count, lane);
+  return d.range();
 }
 
 // Whether a tile of rows and a tile of keys can hide something from each other:
@@ -153,12 +164,85 @@ __device__ __forceinline__ int doc_class(const DocRange& a, const DocRange& b) {
 // ------------------------------------------------------------------ scores
 
 // A raw product q.k to a score in log2 units: capped, then lowered by the distance.
-//   cap:  cap tanh(scale qk / cap) = cap - 2 cap / (1 + exp(2 scale qk / cap)), whose absolute
-//         error (about 2^-22 cap) is what the exponential afterwards feels
-//   bias: -slope |position - key|
-__device__ __forceinline__ float cap_score(float s, const MaskParams& m) {
-  const float e = ex2(s * m.cap_in);
-  return fmaf(-2.f * m.cap_log2, rcp(e + 1.f), m.cap_log2);
+//   cap:  cap tanh(y), y = scale qk / cap.  Where all |y| of a warp's 64 columns are at most 1/2
+//         (scores up to half the cap), tanh comes from y (a0 + a1 y^2 + a2 y^4 + a3 y^6), fitted for
+//         least absolute error (1.3e-7, Lawson's iteratively reweighted least squares), on pairs
+//         on the FMA pipe; else from 1 - 2 / (1 + exp(2 y)) on the special-function unit, whose
+//         absolute error is about 2^-22.  The exponential afterwards feels cap times that.
+//   bias: -slope |position - key|.  With e = (first column's distance, signed), the 64 columns
+//         are at |e + k|; where every row of the warp lies on one side of them that is linear in
+//         k, and the row's part goes into the exponential's reference.
+// (One special-function result per element for the softmax and two for the exact tanh: they
+// bound a capped tile at 3072 cycles, the polynomial at about 1100.)
+constexpr float kTanh0 = 0.99999768f, kTanh1 = -0.33320656f, kTanh2 = 0.13145144f, kTanh3 = -0.043372445f;
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Largest |s| of N values (a NaN wins).
+template <int N>
+__device__ __forceinline__ float abs_max(const uint32_t (&s)[N]) {
+  float mv[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < N; k += 2)
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;"
+        : "=f"(mv[(k >> 1) & 3])
+        : "f"(mv[(k >> 1) & 3]), "f"(__uint_as_float(s[k])), "f"(__uint_as_float(s[k + 1])));
+  return max3_nan(mv[0], mv[1], max3_nan(mv[2], mv[3], mv[3]));
+}
+
+// Raw products to tanh(scale qk / cap), in place; the whole warp takes one way.
+template <int N>
+__device__ __forceinline__ void tanh_scores(uint32_t (&s)[N], const MaskParams& m) {
+  const bool small = abs_max<N>(s) <= m.cap_half;
+  if (__all_sync(0xffffffffu, small)) {
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+      const float2 y = __fmul2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), both(m.cap_in));
+      const float2 z = __fmul2_rn(y, y);
+      float2 p = __ffma2_rn(z, both(kTanh3), both(kTanh2));
+      p = __ffma2_rn(p, z, both(kTanh1));
+      p = __fmul2_rn(__ffma2_rn(p, z, both(kTanh0)), y);
+      s[k] = __float_as_uint(p.x);
+      s[k + 1] = __float_as_uint(p.y);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      s[k] = __float_as_uint(fmaf(-2.f, rcp(ex2(__uint_as_float(s[k]) * (2.f * kLog2e * m.cap_in)) + 1.f), 1.f));
+  }
+}
+
+// Adds the bias to N scores: the columns' distances are |e + k|.  Returns what is still to be
+// added to every score of the row (0 where a row lies inside the columns).
+template <int N>
+__device__ __forceinline__ float add_bias(uint32_t (&s)[N], float slope, int e) {
+  const bool right = __all_sync(0xffffffffu, e >= 0), left = __all_sync(0xffffffffu, e + N - 1 <= 0);
+  if (right || left) {
+    const float b = right ? -slope : slope;
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+      const float2 v = __ffma2_rn(make_float2(static_cast<float>(k), static_cast<float>(k + 1)), both(b),
+                                  make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+      s[k] = __float_as_uint(v.x);
+      s[k + 1] = __float_as_uint(v.y);
+    }
+    return b * static_cast<float>(e);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    s[k] = __float_as_uint(fmaf(-slope, fabsf(static_cast<float>(e) + static_cast<float>(k)), __uint_as_float(s[k])));
+  return 0.f;
+}
+
+// factor * s, on pairs, in place.
+template <int N>
+__device__ __forceinline__ void scale_scores(uint32_t (&s)[N], float factor) {
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    const float2 v = __fmul2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), both(factor));
+    s[k] = __float_as_uint(v.x);
+    s[k + 1] = __float_as_uint(v.y);
+  }
 }
 
 }  // namespace masked

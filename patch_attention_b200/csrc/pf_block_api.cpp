@@ -131,8 +131,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 float scale_of(const pf_masked_attn_config& c) {
   return c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / std::sqrt(static_cast<float>(c.head_dim));
 }
-// 2 scale / cap in units of log2: the exponent of the cap's tanh.
-float cap_in_of(const pf_masked_attn_config& c) { return c.softcap > 0.f ? 2.f * scale_of(c) / c.softcap * kLog2e : 0.f; }
+// scale / cap: a raw product's argument of the cap's tanh.
+float cap_in_of(const pf_masked_attn_config& c) { return c.softcap > 0.f ? scale_of(c) / c.softcap : 0.f; }
 
 pf_status check_masked(const pf_masked_attn_config* c) {
   if (!c) return PF_ERR_INVALID_ARG;
@@ -141,7 +141,7 @@ pf_status check_masked(const pf_masked_attn_config* c) {
   if (c->head_dim != 64 && c->head_dim != 72 && c->head_dim != 128) return PF_ERR_UNSUPPORTED;
   if (!(c->softmax_scale >= 0.f) || std::isinf(c->softmax_scale)) return PF_ERR_INVALID_ARG;
   if (!(c->softcap >= 0.f) || !std::isfinite(c->softcap * kLog2e) || !std::isfinite(scale_of(*c) * kLog2e) ||
-      !std::isfinite(cap_in_of(*c)))
+      !std::isfinite(3.f * cap_in_of(*c)))
     return PF_ERR_INVALID_ARG;
   // CTAs (at most 8 per query tile and head, or per key tile) on a 31-bit grid
   const double longest = c->n_q > c->n_k ? c->n_q : c->n_k;
@@ -169,6 +169,7 @@ pf_status make_mask(const pf_masked_attn_config& c, const float* slopes, const i
   m.scale_log2 = scale_of(c) * kLog2e;
   m.cap_log2 = c.softcap * kLog2e;
   m.cap_in = cap_in_of(c);
+  m.cap_half = c.softcap > 0.f ? 0.5f / m.cap_in : 0.f;
   return PF_OK;
 }
 

@@ -157,7 +157,8 @@ struct MaskParams {
   int causal, n_q, n_k;
   float scale_log2;     // softmax scale * log2(e)
   float cap_log2;       // cap * log2(e); 0: no cap
-  float cap_in;         // 2 scale / cap * log2(e)
+  float cap_in;         // scale / cap
+  float cap_half;       // raw products up to this are below half the cap
 };
 struct MaskedFwdParams {
   CUtensorMap tm_q, tm_k, tm_v;  // 4-D [batch][rows][heads][d]; q's box is pack heads x 128 / pack rows

@@ -150,6 +150,22 @@ def test_documents_of_other_lengths_and_everything_at_once():
     assert torch.equal(o, v.roll(-3, 1))  # each query copies the one value it sees
 
 
+def test_any_negative_id_is_padding():
+    q, k, v = inputs(1, 128, 128, 1, 1, 64, seed=14)
+    doc = torch.zeros(1, 128, device="cuda", dtype=torch.int32)
+    doc[0, 5], doc[0, 77], doc[0, 127] = -2 ** 31, -1, -7
+    check(q, k, v, pa.ScoreRule(doc_q=doc, doc_k=doc))
+
+
+def test_scores_beyond_half_the_cap_and_within():
+    # some rows of a warp take the exponential form of the cap, others alone would not
+    q, k, v = inputs(1, 200, 300, 2, 2, 64, seed=15)
+    for cap in (1.0, 2.0, 8.0, 100.0):
+        check(q, k, v, pa.ScoreRule(softcap=cap))
+    q[:, 40:60] *= 30
+    check(q, k, v, pa.ScoreRule(softcap=8.0, slopes=slopes(2)))
+
+
 def test_no_keys_no_queries():
     q, k, v = inputs(2, 5, 0, 2, 2, 64)
     o, lse = check(q, k, v)
