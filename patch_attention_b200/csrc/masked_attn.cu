@@ -87,14 +87,15 @@ struct Work {
   int rows_per_tile;          // queries of a tile (128 / pack)
   int j0, j1;
   int lim_lo[NQ], lim_hi[NQ];  // key limits of the tile's first and last query; lim_hi -1: sees none
-  const uint8_t* cls;          // documents' classes, 2 bits per query tile, from j0 on; or null
+  const uint8_t* cls;          // documents' classes, 2 bits per query tile, from tile cls0 on; or null
+  int cls0;
 
   // 0: no pair visible, 1: some, 2: every one
   __device__ __forceinline__ int of(int t, int j) const {
     const int k0 = j * kRows;
     if (k0 > (t == 0 ? lim_hi[0] : lim_hi[NQ - 1])) return 0;
     const int c = k0 + kRows - 1 <= (t == 0 ? lim_lo[0] : lim_lo[NQ - 1]) ? 2 : 1;
-    return cls == nullptr ? c : min(c, (cls[j - j0] >> (2 * t)) & 3);
+    return cls == nullptr ? c : min(c, (cls[j - cls0] >> (2 * t)) & 3);
   }
   __device__ __forceinline__ bool any(int j) const {
     bool r = of(0, j) != 0;
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* cls = reinterpret_cast<uint8_t*>(bars) + 512;
+  __shared__ int seen_tiles[2];  // first and last key tile with a document of this CTA's
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -157,8 +159,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
     w.lim_lo[t] = n > 0 ? key_limit(mk, first, prefix) : -1;
     w.lim_hi[t] = n > 0 ? key_limit(mk, first + n - 1, prefix) : -1;
     if (mk.doc_q != nullptr) {
-      qdoc[t] = doc_range(mk.doc_q + static_cast<long long>(w.b) * mk.n_q, first, n, lane);
-      if (qdoc[t].lo > qdoc[t].hi) w.lim_hi[t] = -1;
+      qdoc[t] = {0u, -1, true};
+      if (n > 0) qdoc[t] = doc_range(mk.doc_q + static_cast<long long>(w.b) * mk.n_q + first, n, lane);
+      if (qdoc[t].hi < 0) w.lim_hi[t] = -1;
     }
     lim_max = max(lim_max, w.lim_hi[t]);
   }
@@ -168,6 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
   w.cls = mk.doc_q != nullptr ? cls : nullptr;
 
   if (threadIdx.x == 0) {
+    seen_tiles[0] = INT32_MAX;
+    seen_tiles[1] = -1;
     mbar_init(smem_u32(q_full), 1);
     for (int st = 0; st < S; ++st) {
       mbar_init(smem_u32(kv_full + st), 1);
@@ -200,27 +205,18 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
   }
   if (mk.doc_q != nullptr) {
     const int* ids = mk.doc_k + static_cast<long long>(w.b) * mk.n_k;
-    constexpr int kWarps = kThreads / 32, kAtOnce = 4;
-    for (int j = w.j0 + warp; j < w.j1; j += kWarps * kAtOnce) {
-      DocIds d[kAtOnce];
-#pragma unroll
-      for (int x = 0; x < kAtOnce; ++x) {
-        const int jx = j + x * kWarps;
-        d[x].load(ids, jx * kRows, jx < w.j1 ? mk.n_k - jx * kRows : 0, lane);
-      }
-#pragma unroll
-      for (int x = 0; x < kAtOnce; ++x) {
-        const DocRange r = d[x].range();
-        int c = doc_class(qdoc[0], r);
-        if (NQ == 2) c |= doc_class(qdoc[NQ - 1], r) << 2;
-        if (lane == 0 && j + x * kWarps < w.j1) cls[j + x * kWarps - w.j0] = static_cast<uint8_t>(c);
-      }
-    }
+    __syncthreads();  // seen_tiles is set
+    class_tiles<NQ, kThreads / 32>(ids, mk.n_k, w.j0, w.j1, qdoc, cls, seen_tiles, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  w.cls0 = w.j0;
+  if (mk.doc_q != nullptr) {  // only between the first and the last tile that shares a document
+    w.j1 = min(w.j1, seen_tiles[1] + 1);
+    w.j0 = min(seen_tiles[0], w.j1);
+  }
   // V rows can only be unseen where something hides them
   const bool scrub = mk.causal || mk.doc_q != nullptr;
 

@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* cls = reinterpret_cast<uint8_t*>(bars) + 256;
+  __shared__ int seen_tiles[2];  // first and last streaming tile with a document of this CTA's
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -94,6 +95,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
   const bool docs = mk.doc_q != nullptr;
 
   if (threadIdx.x == 0) {
+    seen_tiles[0] = INT32_MAX;
+    seen_tiles[1] = -1;
     mbar_init(smem_u32(x_full), 1);
     for (int st = 0; st < S; ++st) {
       mbar_init(smem_u32(y_full + st), 1);
@@ -124,24 +127,11 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
     tmem_relinquish();
   }
   if (docs) {
-    const DocRange mine = doc_range((KEYS ? mk.doc_k + bk : mk.doc_q + bq), x0,
-                                    min(kRows, (KEYS ? mk.n_k : mk.n_q) - x0), lane);
-    const int* ids = KEYS ? mk.doc_q + bq : mk.doc_k + bk;
-    const int count = KEYS ? mk.n_q : mk.n_k;
-    constexpr int kWarps = kThreads / 32, kAtOnce = 4;
-    for (int j = warp; j < y_tiles; j += kWarps * kAtOnce) {
-      DocIds d[kAtOnce];
-#pragma unroll
-      for (int x = 0; x < kAtOnce; ++x) {
-        const int jx = j + x * kWarps;
-        d[x].load(ids, jx * kRows, jx < y_tiles ? count - jx * kRows : 0, lane);
-      }
-#pragma unroll
-      for (int x = 0; x < kAtOnce; ++x) {
-        const DocRange r = d[x].range();
-        if (lane == 0 && j + x * kWarps < y_tiles) cls[j + x * kWarps] = static_cast<uint8_t>(doc_class(mine, r));
-      }
-    }
+    const DocRange mine[1] = {doc_range((KEYS ? mk.doc_k + bk : mk.doc_q + bq) + x0,
+                                        min(kRows, (KEYS ? mk.n_k : mk.n_q) - x0), lane)};
+    __syncthreads();  // seen_tiles is set
+    class_tiles<1, kThreads / 32>(KEYS ? mk.doc_q + bq : mk.doc_k + bk, KEYS ? mk.n_q : mk.n_k, 0, y_tiles, mine, cls,
+                                  seen_tiles, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -157,10 +147,22 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
     const int c = k_first + kRows - 1 <= lo ? 2 : 1;
     return docs ? min(c, static_cast<int>(cls[j])) : c;
   };
-  // streaming tiles are walked head by head; `next` finds the first one seen from (g, j) on
+  // streaming tiles [y_lo, y_hi) are walked head by head; `next` finds the first one seen from
+  // (g, j) on
+  int y_lo = 0, y_hi = y_tiles;
+  if (mk.causal) {
+    if (!KEYS)  // the furthest key of the last query
+      y_hi = min(y_hi, (key_limit(mk, min(x0 + kRows, mk.n_q) - 1, prefix) + kRows) / kRows);
+    else if (x0 >= prefix)  // the first query at or behind the first key
+      y_lo = max(x0 - off, 0) / kRows;
+  }
+  if (docs) {
+    y_hi = min(y_hi, seen_tiles[1] + 1);
+    y_lo = max(y_lo, min(seen_tiles[0], y_hi));
+  }
   auto next = [&](int& g, int& j) {
-    for (; g < rounds; ++g, j = 0)
-      for (; j < y_tiles; ++j)
+    for (; g < rounds; ++g, j = y_lo)
+      for (; j < y_hi; ++j)
         if (see(j) != 0) return true;
     return false;
   };
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
     if (warp == kWarpLoad) {
       // ------------------------------------------------------------ TMA producer
       if (lane == 0) {
-        int g = 0, j = 0, i = 0;
+        int g = 0, j = y_lo, i = 0;
         bool ok = true;
         bool more = next(g, j);
         if (more) {  // nothing to do without a tile
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
           for (int kk = 0; kk < 4; ++kk)
             mma_ts(d, a + kk * 8, smem_desc_lo(b0 + static_cast<uint32_t>((kk * 2048) >> 4)), idesc_acc, acc || kk > 0);
         };
-        int g = 0, j = 0, i = 0;
+        int g = 0, j = y_lo, i = 0;
         bool ok = true;
         bool more = next(g, j);
         if (more) {
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
         }
         reach_all = __reduce_max_sync(0xffffffffu, reach_all);
       }
-      int g = 0, j = 0, i = 0;
+      int g = 0, j = y_lo, i = 0;
       bool ok = true;
       for (bool more = next(g, j); more; ++j, more = next(g, j), ++i) {
         const int st = i % S;
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
     }
     float slope = 0.f;
     bool ok = true;
-    int g = 0, j = 0, i = 0, slope_of = -1;
+    int g = 0, j = y_lo, i = 0, slope_of = -1;
     for (bool more = next(g, j); more && ok; ++j, more = next(g, j), ++i) {
       const int st = i % S;
       const int base = j * kRows + h * 64;

@@ -118,47 +118,80 @@ __device__ __forceinline__ uint64_t document_bits(int mine, int id0, int id1) {
   return bits;
 }
 
-// Smallest and largest document of up to 128 ids (negative ones left out), and whether any id was
-// negative.  Whole-warp; lo > hi: no document.  The ids are loaded first, so that several ranges
-// can be in flight.
+// Smallest and largest document of 1 to 128 ids (negative ones left out), and whether any id was
+// negative.  Whole-warp; hi < 0: no document.  The ids are loaded first, so that several ranges
+// can be in flight; past the end the last id is taken again.
 struct DocRange {
-  int lo, hi;
+  unsigned lo;
+  int hi;
   bool gaps;
 };
 struct DocIds {
-  int id[4];  // -1: no document, INT32_MIN: past the end
-  __device__ __forceinline__ void load(const int* ids, int first, int count, int lane) {
+  int id[4];
+  __device__ __forceinline__ void load(const int* ids, int count, int lane) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-      id[x] = x * 32 + lane < count ? max(__ldg(ids + first + x * 32 + lane), -1) : INT32_MIN;
+    for (int x = 0; x < 4; ++x) id[x] = __ldg(ids + min(x * 32 + lane, count - 1));
   }
   __device__ __forceinline__ DocRange range() const {
-    int lo = INT32_MAX, hi = -1;
-    bool gaps = false;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      gaps = gaps || id[x] == -1;
-      lo = min(lo, id[x] < 0 ? INT32_MAX : id[x]);
-      hi = max(hi, id[x]);
-    }
+    // as unsigned numbers the negative ids are the largest
+    const unsigned u[4] = {static_cast<unsigned>(id[0]), static_cast<unsigned>(id[1]), static_cast<unsigned>(id[2]),
+                           static_cast<unsigned>(id[3])};
     DocRange r;
-    r.lo = __reduce_min_sync(0xffffffffu, lo);
-    r.hi = __reduce_max_sync(0xffffffffu, hi);
-    r.gaps = __any_sync(0xffffffffu, gaps);
+    r.lo = __reduce_min_sync(0xffffffffu, min(min(u[0], u[1]), min(u[2], u[3])));
+    r.hi = __reduce_max_sync(0xffffffffu, max(max(id[0], id[1]), max(id[2], id[3])));
+    r.gaps = __any_sync(0xffffffffu, (id[0] | id[1] | id[2] | id[3]) < 0);
     return r;
   }
 };
-__device__ __forceinline__ DocRange doc_range(const int* ids, int first, int count, int lane) {
+__device__ __forceinline__ DocRange doc_range(const int* ids, int count, int lane) {
   DocIds d;
-  d.load(ids, first, count, lane);
+  d.load(ids, count, lane);
   return d.range();
 }
 
 // Whether a tile of rows and a tile of keys can hide something from each other:
 // 0 no pair in common, 1 some pairs, 2 every pair.
 __device__ __forceinline__ int doc_class(const DocRange& a, const DocRange& b) {
-  if (a.lo > a.hi || b.lo > b.hi || a.hi < b.lo || b.hi < a.lo) return 0;
-  return a.lo == a.hi && b.lo == b.hi && a.lo == b.lo && !a.gaps && !b.gaps ? 2 : 1;
+  if (a.hi < 0 || b.hi < 0 || static_cast<unsigned>(a.hi) < b.lo || static_cast<unsigned>(b.hi) < a.lo) return 0;
+  return a.lo == b.lo && a.hi == b.hi && a.lo == static_cast<unsigned>(a.hi) && !a.gaps && !b.gaps ? 2 : 1;
+}
+
+// Classes of tiles [j0, j1) of ids (`count` of them from the start) against NQ ranges, 2 bits each,
+// into cls[j - j0]; the first and the last tile that any of them sees into range[0], range[1]
+// (shared; range[0] > range[1]: none).  By all warps of the block, followed by a barrier.  All of a
+// warp's loads are in flight at once: a pass over the ids of every tile costs every CTA about
+// one memory latency.
+template <int NQ, int WARPS>
+__device__ __forceinline__ void class_tiles(const int* ids, int count, int j0, int j1, const DocRange (&q)[NQ],
+                                            uint8_t* cls, int* range, int warp, int lane) {
+  constexpr int kAtOnce = 8;
+  int first = INT32_MAX, last = -1;
+  for (int j = j0 + warp; j < j1; j += WARPS * kAtOnce) {
+    DocIds d[kAtOnce];
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      const int jx = min(j + x * WARPS, j1 - 1);
+      d[x].load(ids + static_cast<long long>(jx) * kRows, min(kRows, count - jx * kRows), lane);
+    }
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      const int jx = j + x * WARPS;
+      const DocRange r = d[x].range();
+      int c = doc_class(q[0], r);
+      if (NQ == 2) c |= doc_class(q[NQ - 1], r) << 2;
+      if (jx < j1) {
+        if (lane == 0) cls[jx - j0] = static_cast<uint8_t>(c);
+        if (c != 0) {
+          first = min(first, jx);
+          last = jx;
+        }
+      }
+    }
+  }
+  if (lane == 0 && last >= 0) {
+    atomicMin(range, first);
+    atomicMax(range + 1, last);
+  }
 }
 
 // ------------------------------------------------------------------ scores
