@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kWarpLoad) {
       // ------------------------------------------------------------ TMA producer
-      if (lane == 0) {
+      if (elect_one()) {
         const uint32_t qbar = smem_u32(q_full);
         const uint32_t q_bytes = static_cast<uint32_t>(w.rows_per_tile * p.pack) * 128u * Dm::kChunks;
         mbar_arrive_expect_tx(qbar, NQ * q_bytes);
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
       }
     } else if (warp == kWarpMma || (NQ == 2 && warp == kWarpMma2)) {
       // ------------------------------------------------------------ MMA issuer of query tile t
-      if (lane == 0) {
+      if (elect_one()) {
         const int t = warp == kWarpMma ? 0 : 1;
         constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 64, 0);         // N = 64 keys
         constexpr uint32_t idesc_pv = idesc_bf16_f32(128, Dm::kMmaN, 1);  // N = head_dim (padded)

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
   if (warp >= 8) {
     if (warp == kWarpLoad) {
       // ------------------------------------------------------------ TMA producer
-      if (lane == 0) {
+      if (elect_one()) {
         int g = 0, j = y_lo, i = 0;
         bool ok = true;
         bool more = next(g, j);
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
       }
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, 0);           // N = 64 streaming rows
         constexpr uint32_t idesc_acc = idesc_bf16_f32(128, Dm::kMmaN, 1);  // N = head_dim (padded)
         const uint32_t x_lo = desc_start(smem_u32(sX)) | desc_lbo_bits(16);

@@ -28,6 +28,19 @@ struct Dims {
   static constexpr int kTileBytes = kChunks * kChunkBytes;
 };
 
+// One lane of a converged warp.  Unlike a test of the lane number it tells the compiler that the
+// code behind it is one thread's, so that the operands of TMA and MMA instructions are computed
+// in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void raise_abort(volatile int* abort, unsigned* watchdog, unsigned code) {
   *abort = 1;
   atomicOr(watchdog, code);
