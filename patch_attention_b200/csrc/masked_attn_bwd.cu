@@ -12,12 +12,19 @@
 // and the sums have one order.  The price is that s and do.v are computed twice: 7 matrix products
 // instead of 5.
 //
-// With X1, X2 the staying and Y1, Y2 the streaming tiles, for each 64-row half h of a Y tile:
-//   S_h = X1 Y1_h^T, dP_h = X2 Y2_h^T into TMEM; a softmax warpgroup (one thread per staying row) turns
-//   them into P_h and dS_h, written back over them as bf16;  accV += P_h Y2_h (keys stay only),
-//   accK += dS_h Y1_h with P_h, dS_h as the TMEM operand and Y as an MN-major operand from shared memory.
-// One warpgroup works on each half, so the tensor core runs the products of one half while the other
-// is exponentiated.  P and dS are rounded to bf16, the operand type; everything else is fp32.
+// With X1, X2 the staying and Y1, Y2 the streaming tiles (128 rows each):
+//   S = X1 Y1^T, dP = X2 Y2^T into TMEM; two softmax warpgroups, each for 64 of the streaming rows (one
+//   thread per staying row), turn them into P and dS, both written back over dP as bf16;
+//   accV += P Y2 (keys stay only), accK += dS Y1 with P, dS as the TMEM operand and Y as an MN-major
+//   operand from shared memory.
+// S's columns are free as soon as they are in registers, so the next tile's S is computed under this
+// one's exponentials, and dV, dK and the next dP under the next exponentials: with P written over S
+// a chain ran through all four products (5600 cycles per tile at head_dim 128).  An MMA costs about
+// 80 cycles or its 128 x N x 16 share of the tensor rate, whichever is more, so S and dP are made 128
+// columns wide (64 at N = 128) and not per warpgroup (84 measured at N = 64, where 32 would do).  The
+// two halves of a streaming tile are loaded and freed apart: two whole tiles fill the shared
+// memory at head_dim 128, and half a tile's start is gained for the loads.  P and dS are rounded to
+// bf16, the operand type; everything else is fp32.
 //
 // Streaming rows whose product with a zero probability must not be NaN -- queries that see nothing
 // (lse = -inf), keys that no query of the tile sees -- are zeroed in shared memory first.
@@ -32,19 +39,20 @@ namespace {
 using namespace masked;
 
 constexpr int kThreads = 384;  // warps 0-3, 4-7: softmax of half 0, 1; then MMA, TMA, helper
+constexpr int kUnit = 64;      // rows of half a streaming tile
 constexpr int kWarpMma = 8;
 constexpr int kWarpLoad = 9;
 constexpr int kWarpHelp = 10;
-constexpr uint32_t kColDp = 128;    // S_h at 64 h, dP_h at 128 + 64 h
+constexpr uint32_t kColDp = 128;    // warpgroup h: S at 64 h, dP at 128 + 64 h (then dS, P: 32 columns each)
 constexpr uint32_t kColAccK = 256;  // dK or dQ
 constexpr uint32_t kColAccV = 384;  // dV
 
 template <int D>
-constexpr int kStages = D <= 64 ? 4 : 2;  // (Y1, Y2) pairs in flight
+constexpr int kStages = D <= 64 ? 4 : 2;  // streaming tiles (Y1, Y2) in flight
 
 template <int D>
 constexpr int smem_bytes(int cls_bytes) {
-  return 1024 + (2 + 2 * kStages<D>)*Dims<D>::kTileBytes + kStages<D> * kRows * 8 + 256 + cls_bytes;
+  return 1024 + (2 + 2 * kStages<D>)*Dims<D>::kTileBytes + kStages<D> * (kRows * 8 + 16) + 512 + cls_bytes;
 }
 
 // KEYS: keys stay (dK, dV), else queries stay (dQ).  MOD: scores are capped or biased.
@@ -56,21 +64,25 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sX = smem;                       // X1, X2
+  constexpr int R = 2 * S;  // half tiles in flight: stage i / 2, half i % 2
   uint8_t* sY = smem + 2 * Dm::kTileBytes;  // [stage] Y1, Y2
-  float* stat = reinterpret_cast<float*>(sY + 2 * S * Dm::kTileBytes);  // [stage] -lse[128] (log2), -delta[128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stat + S * 2 * kRows);
+  float* stat = reinterpret_cast<float*>(sY + 2 * S * Dm::kTileBytes);  // [half tile] -lse[64] (log2), -delta[64]
+  // [stage] the tile's place among the streaming tiles (-1: none is left), its query head among
+  // those that stream, and how it is seen (1 in part, 2 entirely): written by the helper
+  int4* info = reinterpret_cast<int4*>(stat + R * 2 * kUnit);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(info + S);
   uint64_t* x_full = bars;
   uint64_t* y_full = bars + 1;
-  uint64_t* y_empty = y_full + S;
-  uint64_t* y_ok = y_empty + S;
-  uint64_t* s_full = y_ok + S;    // [h]
-  uint64_t* dp_full = s_full + 2;
-  uint64_t* pt_full = dp_full + 2;
-  uint64_t* ds_full = pt_full + 2;
+  uint64_t* y_empty = y_full + R;  // [half tile], as y_full, y_ok
+  uint64_t* y_ok = y_empty + R;
+  uint64_t* s_full = y_ok + R;
+  uint64_t* dp_full = s_full + 1;
+  uint64_t* s_free = dp_full + 1;  // [warpgroup] its S is in registers
+  uint64_t* ds_full = s_free + 2;  // [warpgroup] its P and dS are written
   uint64_t* acc_full = ds_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint8_t* cls = reinterpret_cast<uint8_t*>(bars) + 256;
+  uint8_t* cls = reinterpret_cast<uint8_t*>(bars) + 512;
   __shared__ int seen_tiles[2];  // first and last streaming tile with a document of this CTA's
 
   const int warp = threadIdx.x >> 5;
@@ -98,15 +110,15 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
     seen_tiles[0] = INT32_MAX;
     seen_tiles[1] = -1;
     mbar_init(smem_u32(x_full), 1);
-    for (int st = 0; st < S; ++st) {
-      mbar_init(smem_u32(y_full + st), 1);
-      mbar_init(smem_u32(y_empty + st), 1);
-      mbar_init(smem_u32(y_ok + st), 1);
+    for (int r = 0; r < R; ++r) {
+      mbar_init(smem_u32(y_full + r), 1);
+      mbar_init(smem_u32(y_empty + r), 1);
+      mbar_init(smem_u32(y_ok + r), 1);
     }
+    mbar_init(smem_u32(s_full), 1);
+    mbar_init(smem_u32(dp_full), 1);
     for (int h = 0; h < 2; ++h) {
-      mbar_init(smem_u32(s_full + h), 1);
-      mbar_init(smem_u32(dp_full + h), 1);
-      mbar_init(smem_u32(pt_full + h), 4);
+      mbar_init(smem_u32(s_free + h), 4);
       mbar_init(smem_u32(ds_full + h), 4);
     }
     mbar_init(smem_u32(acc_full), 1);
@@ -166,12 +178,14 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
         if (see(j) != 0) return true;
     return false;
   };
+  // Y1 (which = 0) or Y2 of half tile r: chunk c's 64 rows are at + c * kChunkBytes
+  auto half_tile = [&](int r, int which) { return sY + (r & ~1) * Dm::kTileBytes + which * Dm::kTileBytes + (r & 1) * kUnit * 128; };
 
   if (warp >= 8) {
     if (warp == kWarpLoad) {
       // ------------------------------------------------------------ TMA producer
       if (elect_one()) {
-        int g = 0, j = y_lo, i = 0;
+        int g = 0, j = y_lo, i = 0;  // i: half tiles
         bool ok = true;
         bool more = next(g, j);
         if (more) {  // nothing to do without a tile
@@ -183,91 +197,101 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
           }
         }
         const bool any = more;
-        for (; more && ok; ++j, more = next(g, j), ++i) {
-          const int st = i % S;
-          if (!(ok = mbar_wait(smem_u32(y_empty + st), ((i / S) & 1) ^ 1, abort, kWaitNs))) break;
-          const uint32_t yb = smem_u32(y_full + st);
-          mbar_arrive_expect_tx(yb, 2 * Dm::kTileBytes);
-          for (int c = 0; c < Dm::kChunks; ++c) {
-            uint8_t* y = sY + 2 * st * Dm::kTileBytes + c * kChunkBytes;
-            tma_load_4d(smem_u32(y), &p.tm_y1, c * 64, y_head + g, j * kRows, b, yb);
-            tma_load_4d(smem_u32(y + Dm::kTileBytes), &p.tm_y2, c * 64, y_head + g, j * kRows, b, yb);
+        for (; more && ok; ++j, more = next(g, j))
+          for (int h = 0; h < 2; ++h, ++i) {
+            const int r = i % R;
+            if (!(ok = mbar_wait(smem_u32(y_empty + r), ((i / R) & 1) ^ 1, abort, kWaitNs))) break;
+            const uint32_t yb = smem_u32(y_full + r);
+            mbar_arrive_expect_tx(yb, Dm::kTileBytes);
+            for (int which = 0; which < 2; ++which)
+              for (int c = 0; c < Dm::kChunks; ++c)
+                tma_load_4d(smem_u32(half_tile(r, which) + c * kChunkBytes), which ? &p.tm_y2 : &p.tm_y1, c * 64, y_head + g,
+                            j * kRows + h * kUnit, b, yb);
           }
-        }
         if (!ok) raise_abort(abort, p.watchdog, kWdLoad);
         // drain: every issued copy must land before the CTA exits
         if (any) mbar_wait(smem_u32(x_full), 0, nullptr, kWaitNs);
-        for (int k = i > S ? i - S : 0; k < i; ++k)
-          mbar_wait(smem_u32(y_full + k % S), (k / S) & 1, nullptr, kWaitNs);
+        for (int k = i > R ? i - R : 0; k < i; ++k)
+          mbar_wait(smem_u32(y_full + k % R), (k / R) & 1, nullptr, kWaitNs);
       }
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------ MMA issuer
       if (elect_one()) {
-        constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, 0);           // N = 64 streaming rows
+        constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0);          // N = 128 streaming rows
         constexpr uint32_t idesc_acc = idesc_bf16_f32(128, Dm::kMmaN, 1);  // N = head_dim (padded)
         const uint32_t x_lo = desc_start(smem_u32(sX)) | desc_lbo_bits(16);
         const uint32_t yk_lo = desc_start(smem_u32(sY)) | desc_lbo_bits(16);
         const uint32_t yn_lo = desc_start(smem_u32(sY)) | desc_lbo_bits(kChunkBytes);
-        // which = 0: S_h = X1 Y1_h^T, 1: dP_h = X2 Y2_h^T
-        auto product = [=](int which, int h, int st) {
+        // tile i, which = 0: S = X1 Y1^T, 1: dP = X2 Y2^T
+        auto product = [=](int which, int i) {
           const uint32_t a0 = x_lo + static_cast<uint32_t>((which * Dm::kTileBytes) >> 4);
-          const uint32_t b0 = yk_lo + static_cast<uint32_t>(((2 * st + which) * Dm::kTileBytes + h * 8192) >> 4);
-          const uint32_t d = tmem + which * kColDp + h * 64;
+          const uint32_t b0 = yk_lo + static_cast<uint32_t>(((2 * (i % S) + which) * Dm::kTileBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < Dm::kMmaN / 16; ++kk) {
             const uint32_t o = static_cast<uint32_t>(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
-            mma_ss(d, smem_desc_lo(a0 + o), smem_desc_lo(b0 + o), idesc_s, kk > 0);
+            mma_ss(tmem + which * kColDp, smem_desc_lo(a0 + o), smem_desc_lo(b0 + o), idesc_s, kk > 0);
           }
+          mma_commit(smem_u32(which ? dp_full : s_full));
         };
-        // which = 0: accK += dS_h Y1_h, 1: accV += P_h Y2_h
-        auto accumulate = [=](int which, int h, int st, bool acc) {
-          const uint32_t b0 = yn_lo + static_cast<uint32_t>(((2 * st + which) * Dm::kTileBytes + h * 8192) >> 4);
+        // half h of tile i, which = 0: accK += dS Y1, 1: accV += P Y2
+        auto accumulate = [=](int which, int h, int i) {
+          const uint32_t b0 = yn_lo + static_cast<uint32_t>(((2 * (i % S) + which) * Dm::kTileBytes + h * kUnit * 128) >> 4);
           const uint32_t d = tmem + (which ? kColAccV : kColAccK);
-          const uint32_t a = tmem + (which ? 0 : kColDp) + h * 64;
+          const uint32_t a = tmem + kColDp + h * 64 + which * 32;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ts(d, a + kk * 8, smem_desc_lo(b0 + static_cast<uint32_t>((kk * 2048) >> 4)), idesc_acc, acc || kk > 0);
+            mma_ts(d, a + kk * 8, smem_desc_lo(b0 + static_cast<uint32_t>((kk * 2048) >> 4)), idesc_acc,
+                   i > 0 || h > 0 || kk > 0);
         };
-        int g = 0, j = y_lo, i = 0;
-        bool ok = true;
-        bool more = next(g, j);
+        // Tile i's dV, dK and tile i + 1's S are issued as they become possible, in either order: with
+        // two tiles in shared memory the next one's rows may come late, and dV, dK free the rows of
+        // the one after.
+        bool ok = mbar_wait(smem_u32(y_ok + 1), 0, abort, kWaitNs);
+        const bool more = ok && info[0].x >= 0;
         if (more) {
-          ok = mbar_wait(smem_u32(x_full), 0, abort, kWaitNs) && mbar_wait(smem_u32(y_ok), 0, abort, kWaitNs);
+          ok = mbar_wait(smem_u32(x_full), 0, abort, kWaitNs);
           if (ok) {
             tc_fence_after();
-            for (int h = 0; h < 2; ++h) {
-              product(0, h, 0);
-              mma_commit(smem_u32(s_full + h));
-              product(1, h, 0);
-              mma_commit(smem_u32(dp_full + h));
-            }
+            product(0, 0);
+            product(1, 0);
           }
         }
-        while (more && ok) {
-          ++j;
-          more = next(g, j);
-          const int st = i % S, sn = (i + 1) % S;
-          for (int h = 0; h < 2 && ok; ++h) {
-            if (KEYS) {
-              if (!(ok = mbar_wait(smem_u32(pt_full + h), i & 1, abort, kWaitNs))) break;
-              tc_fence_after();
-              accumulate(1, h, st, i > 0 || h > 0);
+        for (int i = 0; more && ok; ++i) {
+          const int n = 2 * (i + 1) + 1;  // the next tile's second half
+          const uint32_t full = (n / R) & 1, turn = i & 1;
+          bool begun = false, last = false;
+          int done = 0;  // halves accumulated
+          uint64_t t0 = 0;
+          while (!(begun || last) || done < 2) {
+            bool progress = false;
+            if (!begun && !last && mbar_test(smem_u32(y_ok + n % R), full)) {
+              if (info[(i + 1) % S].x < 0) {
+                last = progress = true;
+              } else if (mbar_test(smem_u32(s_free), turn) && mbar_test(smem_u32(s_free + 1), turn)) {
+                tc_fence_after();
+                product(0, i + 1);
+                begun = progress = true;
+              }
             }
-            if (!(ok = mbar_wait(smem_u32(ds_full + h), i & 1, abort, kWaitNs))) break;
-            tc_fence_after();
-            accumulate(0, h, st, i > 0 || h > 0);
-            if (more) {
-              if (h == 0 && !(ok = mbar_wait(smem_u32(y_ok + sn), ((i + 1) / S) & 1, abort, kWaitNs))) break;
+            if (done < 2 && mbar_test(smem_u32(ds_full + done), turn)) {
               tc_fence_after();
-              product(0, h, sn);
-              mma_commit(smem_u32(s_full + h));
-              product(1, h, sn);
-              mma_commit(smem_u32(dp_full + h));
+              accumulate(0, done, i);
+              if (KEYS) accumulate(1, done, i);
+              mma_commit(smem_u32(y_empty + (2 * i + done) % R));
+              ++done;
+              progress = true;
+            }
+            if (progress) {
+              t0 = 0;
+            } else if (t0 == 0) {
+              t0 = globaltimer_ns();
+            } else if (*abort || globaltimer_ns() - t0 > kWaitNs) {
+              ok = false;
+              break;
             }
           }
-          if (!ok) break;
-          mma_commit(smem_u32(y_empty + st));
-          ++i;
+          if (!ok || last) break;
+          product(1, i + 1);
         }
         if (!ok) raise_abort(abort, p.watchdog, kWdMma);
         // every MMA of this thread: the accumulators are complete, and TMEM may be released
@@ -290,32 +314,52 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
         }
         reach_all = __reduce_max_sync(0xffffffffu, reach_all);
       }
-      int g = 0, j = y_lo, i = 0;
+      // keys stay: the statistics of a half tile's queries, loaded one half tile ahead
+      float l[2], dl[2];
+      auto fetch = [&](int g, int j, int h) {
+        const long long row = (static_cast<long long>(b) * p.heads_q + y_head + g) * mk.n_q;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int query = j * kRows + h * kUnit + x * 32 + lane;
+          l[x] = query < mk.n_q ? __ldg(p.lse + row + query) : -INFINITY;
+          dl[x] = query < mk.n_q ? __ldg(p.delta + row + query) : 0.f;
+        }
+      };
+      int g = 0, j = y_lo, i = 0;  // i: half tiles
       bool ok = true;
-      for (bool more = next(g, j); more; ++j, more = next(g, j), ++i) {
-        const int st = i % S;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(y_empty + st), ((i / S) & 1) ^ 1, abort, kWaitNs));
-        if (!ok) break;
-        bool unseen[4];
-        if (KEYS) {
-          const long long row = (static_cast<long long>(b) * p.heads_q + y_head + g) * mk.n_q;
-          float* out = stat + st * 2 * kRows;
+      bool more = next(g, j);
+      int kind = more ? see(j) : 0;
+      if (KEYS && more) fetch(g, j, 0);
+      while (more && ok) {
+        const int here = j, head = g, seen = kind;
+        const bool partly = !KEYS && seen == 1;
+        for (int h = 0; h < 2; ++h, ++i) {
+          const int r = i % R;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(y_empty + r), ((i / R) & 1) ^ 1, abort, kWaitNs));
+          if (!ok) break;
+          bool unseen[2] = {false, false};
+          if (KEYS) {
+            float* out = stat + r * 2 * kUnit;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int query = j * kRows + x * 32 + lane;
-            const float l = query < mk.n_q ? __ldg(p.lse + row + query) : -INFINITY;
-            unseen[x] = l == -INFINITY;
-            // a query that sees nothing: exp2(s - inf) = 0
-            out[x * 32 + lane] = unseen[x] ? -INFINITY : -l * kLog2e;
-            out[kRows + x * 32 + lane] = unseen[x] ? 0.f : -__ldg(p.delta + row + query);
+            for (int x = 0; x < 2; ++x) {
+              unseen[x] = l[x] == -INFINITY;
+              // a query that sees nothing: exp2(s - inf) = 0
+              out[x * 32 + lane] = unseen[x] ? -INFINITY : -l[x] * kLog2e;
+              out[kUnit + x * 32 + lane] = unseen[x] ? 0.f : -dl[x];
+            }
           }
-        } else {
-          const bool partly = see(j) == 1;
+          if (h == 1) {
+            // (both warpgroups are done with the stage's last tile once its second half is free)
+            if (lane == 0) info[(i / 2) % S] = make_int4(here, head, seen, 0);
+            ++j;
+            more = next(g, j);
+            kind = more ? see(j) : 0;
+          }
+          if (KEYS && more) fetch(g, j, h ^ 1);
+          if (partly) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = j * kRows + x * 32 + lane;
-            unseen[x] = false;
-            if (partly) {
+            for (int x = 0; x < 2; ++x) {
+              const int key = here * kRows + h * kUnit + x * 32 + lane;
               unseen[x] = key > reach_all;
               if (docs) {
                 // the furthest key that a query of this key's document sees, one id at a time
@@ -336,24 +380,32 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
               }
             }
           }
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(y_full + st), (i / S) & 1, abort, kWaitNs));
-        if (!ok) break;
-        bool wrote = false;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(y_full + r), (i / R) & 1, abort, kWaitNs));
+          if (!ok) break;
+          if (__any_sync(0xffffffffu, unseen[0] || unseen[1])) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (unseen[x]) {
-            wrote = true;
-            uint4* r = reinterpret_cast<uint4*>(sY + 2 * st * Dm::kTileBytes + (x * 32 + lane) * 128);
+            for (int x = 0; x < 2; ++x) {
+              if (!unseen[x]) continue;
 #pragma unroll
-            for (int c = 0; c < 2 * Dm::kChunks; ++c)
+              for (int c = 0; c < 2 * Dm::kChunks; ++c) {
+                uint4* to = reinterpret_cast<uint4*>(half_tile(r, c & 1) + (c >> 1) * kChunkBytes + (x * 32 + lane) * 128);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) r[c * (kChunkBytes / 16) + e] = make_uint4(0, 0, 0, 0);
+                for (int e = 0; e < 8; ++e) to[e] = make_uint4(0, 0, 0, 0);
+              }
+            }
+            fence_proxy_async_smem();
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(y_ok + r));
         }
-        if (wrote) fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(y_ok + st));
+      }
+      if (ok) {  // no tile is left
+        const int r = (i + 1) % R;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(y_empty + r), (((i + 1) / R) & 1) ^ 1, abort, kWaitNs));
+        if (ok && lane == 0) {
+          info[(i / 2) % S] = make_int4(-1, 0, 0, 0);
+          mbar_arrive(smem_u32(y_ok + r));
+        }
       }
       if (!ok && lane == 0) raise_abort(abort, p.watchdog, kWdScrub);
     }
@@ -381,12 +433,18 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
     }
     float slope = 0.f;
     bool ok = true;
-    int g = 0, j = y_lo, i = 0, slope_of = -1;
-    for (bool more = next(g, j); more && ok; ++j, more = next(g, j), ++i) {
-      const int st = i % S;
-      const int base = j * kRows + h * 64;
+    int i = 0, slope_of = -1;
+    for (;; ++i) {
+      const int r = (2 * i + h) % R;
+      // the tile's place (and the statistics of both halves) come with its second half
+      ok = mbar_wait(smem_u32(y_ok + (2 * i + 1) % R), ((2 * i + 1) / R) & 1, abort, kWaitNs);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int4 tile = info[i % S];
+      if (tile.x < 0) break;
+      const int g = tile.y, base = tile.x * kRows + h * kUnit;
       uint64_t bits = ~0ull;
-      const bool partly = see(j) == 1;
+      const bool partly = tile.z == 1;
       if (partly) {
         if (KEYS) {
           // queries from row - off on see this key; all of them where it lies in the prefix
@@ -407,112 +465,105 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
         slope = __ldg(mk.slopes + (KEYS ? y_head + g : x_head)) * kLog2e;
         slope_of = g;
       }
-      if (KEYS) ok = mbar_wait(smem_u32(y_ok + st), (i / S) & 1, abort, kWaitNs);  // the statistics
-      ok = ok && mbar_wait(smem_u32(s_full + h), i & 1, abort, kWaitNs);
+      ok = mbar_wait(smem_u32(s_full), i & 1, abort, kWaitNs);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const float* st_lse = stat + st * 2 * kRows + h * 64;
-      float2 pd[32];  // p, times 1 - tanh^2 with a cap
-#pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t s[32], pk[16];
-        tmem_ld32(tS + c0, s);
+      const float* neg = stat + r * 2 * kUnit;  // the columns' -lse, then -delta
+      float2 pd[32];    // p, times 1 - tanh^2 with a cap
+      uint32_t pk[32];  // p as bf16
+      {
+        uint32_t s[64];
+        tmem_ld32(tS, s);
+        tmem_ld32(tS + 32, s + 32);
         tmem_wait_ld();
-        reg_fence<32>(s);
+        reg_fence<64>(s);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(s_free + h));
         float rest = 0.f;
-        float2 damp[16];
         if constexpr (MOD) {
           if (mk.cap_log2 > 0.f) {
-            tanh_scores<32>(s, mk);
+            tanh_scores<64>(s, mk);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 32; ++k) {
               const float2 t = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
-              damp[k] = __ffma2_rn(make_float2(-t.x, -t.y), t, both(1.f));
+              pd[k] = __ffma2_rn(make_float2(-t.x, -t.y), t, both(1.f));
             }
           } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) damp[k] = both(1.f);
+            for (int k = 0; k < 32; ++k) pd[k] = both(1.f);
           }
-          scale_scores<32>(s, mk.cap_log2 > 0.f ? mk.cap_log2 : mk.scale_log2);
-          if (mk.slopes != nullptr) rest = add_bias<32>(s, slope, base + c0 + (KEYS ? off - row : -off - row));
+          scale_scores<64>(s, mk.cap_log2 > 0.f ? mk.cap_log2 : mk.scale_log2);
+          if (mk.slopes != nullptr) rest = add_bias<64>(s, slope, base + (KEYS ? off - row : -off - row));
+        }
+        if (partly) {
+          const uint32_t lo = static_cast<uint32_t>(bits), hi = static_cast<uint32_t>(bits >> 32);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (!(lo >> k & 1u)) s[k] = __float_as_uint(-INFINITY);
+            if (!(hi >> k & 1u)) s[k + 32] = __float_as_uint(-INFINITY);
+          }
+          if constexpr (MOD) {  // the cap's factor of a hidden score may be NaN
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              if (!(bits >> (2 * k) & 1ull)) pd[k].x = 0.f;
+              if (!(bits >> (2 * k + 1) & 1ull)) pd[k].y = 0.f;
+            }
+          }
         }
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
+        for (int k = 0; k < 32; k += 2) {
           float2 ref[2] = {both(neg_lse), both(neg_lse)};
           if (KEYS) {
-            const float4 l = *reinterpret_cast<const float4*>(st_lse + c0 + 2 * k);
+            const float4 l = *reinterpret_cast<const float4*>(neg + 2 * k);
             ref[0] = make_float2(l.x, l.y);
             ref[1] = make_float2(l.z, l.w);
           }
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float2 x = make_float2(__uint_as_float(s[2 * (k + u)]), __uint_as_float(s[2 * (k + u) + 1]));
-            const float2 y = MOD ? __fadd2_rn(__fadd2_rn(x, both(rest)), ref[u]) : __ffma2_rn(x, both(mk.scale_log2), ref[u]);
-            pd[c0 / 2 + k + u] = make_float2(ex2(y.x), ex2(y.y));
+          for (int v = 0; v < 2; ++v) {
+            const float2 x = make_float2(__uint_as_float(s[2 * (k + v)]), __uint_as_float(s[2 * (k + v) + 1]));
+            const float2 y = MOD ? __fadd2_rn(__fadd2_rn(x, both(rest)), ref[v]) : __ffma2_rn(x, both(mk.scale_log2), ref[v]);
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            if (KEYS) pk[k + v] = pack2(e.x, e.y);
+            pd[k + v] = MOD ? __fmul2_rn(pd[k + v], e) : e;
           }
         }
-        if (partly) {
-          const uint32_t mask = static_cast<uint32_t>(bits >> c0);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            if (!(mask >> (2 * k) & 1u)) pd[c0 / 2 + k].x = 0.f;
-            if (!(mask >> (2 * k + 1) & 1u)) pd[c0 / 2 + k].y = 0.f;
-          }
-        }
-        if (KEYS) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) pk[k] = pack2(pd[c0 / 2 + k].x, pd[c0 / 2 + k].y);
-          tmem_st16(tS + c0 / 2, pk);
-        }
-        if constexpr (MOD) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) pd[c0 / 2 + k] = __fmul2_rn(pd[c0 / 2 + k], damp[k]);
-        }
       }
-      if (KEYS) {
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(pt_full + h));
-      }
-      ok = mbar_wait(smem_u32(dp_full + h), i & 1, abort, kWaitNs);
+      ok = mbar_wait(smem_u32(dp_full), i & 1, abort, kWaitNs);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
       for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t dp[32], pk[16];
+        uint32_t dp[32], ds[16];
         tmem_ld32(tP + c0, dp);
         tmem_wait_ld();
         reg_fence<32>(dp);
-        float2 e[16];
+        if (partly) {  // a hidden value may make dp NaN: p = 0 there would not be enough
+          const uint32_t mask = static_cast<uint32_t>(bits >> c0);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!(mask >> k & 1u)) dp[k] = 0u;
+        }
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
           float2 ref[2] = {both(neg_delta), both(neg_delta)};
           if (KEYS) {
-            const float4 l = *reinterpret_cast<const float4*>(st_lse + kRows + c0 + 2 * k);
+            const float4 l = *reinterpret_cast<const float4*>(neg + kUnit + c0 + 2 * k);
             ref[0] = make_float2(l.x, l.y);
             ref[1] = make_float2(l.z, l.w);
           }
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float2 x = make_float2(__uint_as_float(dp[2 * (k + u)]), __uint_as_float(dp[2 * (k + u) + 1]));
-            e[k + u] = __fmul2_rn(pd[c0 / 2 + k + u], __fadd2_rn(x, ref[u]));
+          for (int v = 0; v < 2; ++v) {
+            const float2 x = make_float2(__uint_as_float(dp[2 * (k + v)]), __uint_as_float(dp[2 * (k + v) + 1]));
+            const float2 e = __fmul2_rn(pd[c0 / 2 + k + v], __fadd2_rn(x, ref[v]));
+            ds[k + v] = pack2(e.x, e.y);
           }
         }
-        if (partly) {  // also where a hidden value makes dp NaN
-          const uint32_t mask = static_cast<uint32_t>(bits >> c0);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            if (!(mask >> (2 * k) & 1u)) e[k].x = 0.f;
-            if (!(mask >> (2 * k + 1) & 1u)) e[k].y = 0.f;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) pk[k] = pack2(e[k].x, e[k].y);
-        tmem_st16(tP + c0 / 2, pk);
+        tmem_st16(tP + c0 / 2, ds);  // below the columns still to be read
       }
+      if (KEYS) tmem_st32(tP + 32, pk);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -611,7 +662,7 @@ cudaError_t launch(const MaskedBwdParams& p, cudaStream_t stream) {
 }
 
 template <int D, bool MOD>
-cudaError_t launch_dim(MaskedBwdParams& p, const CUtensorMap (&maps)[4], cudaStream_t stream) {
+cudaError_t launch_dim(MaskedBwdParams& p, const CUtensorMap (&maps)[2][4], cudaStream_t stream) {
   const long long vectors = static_cast<long long>(p.batch) * p.m.n_q * p.heads_q;
   if (vectors > 0) {
     const long long blocks = (vectors * (D <= 64 ? 8 : 16) + 255) / 256;
@@ -620,22 +671,22 @@ cudaError_t launch_dim(MaskedBwdParams& p, const CUtensorMap (&maps)[4], cudaStr
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  p.tm_x1 = maps[1];  // K, V stay; Q, dO stream
-  p.tm_x2 = maps[2];
-  p.tm_y1 = maps[0];
-  p.tm_y2 = maps[3];
+  p.tm_x1 = maps[0][1];  // K, V stay; Q, dO stream
+  p.tm_x2 = maps[0][2];
+  p.tm_y1 = maps[1][0];
+  p.tm_y2 = maps[1][3];
   const cudaError_t e = launch<D, true, MOD>(p, stream);
   if (e != cudaSuccess) return e;
-  p.tm_x1 = maps[0];  // Q, dO stay; K, V stream
-  p.tm_x2 = maps[3];
-  p.tm_y1 = maps[1];
-  p.tm_y2 = maps[2];
+  p.tm_x1 = maps[0][0];  // Q, dO stay; K, V stream
+  p.tm_x2 = maps[0][3];
+  p.tm_y1 = maps[1][1];
+  p.tm_y2 = maps[1][2];
   return launch<D, false, MOD>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_masked_bwd(MaskedBwdParams& p, const CUtensorMap (&maps)[4], cudaStream_t stream) {
+cudaError_t launch_masked_bwd(MaskedBwdParams& p, const CUtensorMap (&maps)[2][4], cudaStream_t stream) {
   const bool mod = p.m.cap_log2 > 0.f || p.m.slopes != nullptr;
   switch (p.head_dim) {
     case 64: return mod ? launch_dim<64, true>(p, maps, stream) : launch_dim<64, false>(p, maps, stream);

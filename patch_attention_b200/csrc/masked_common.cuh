@@ -28,6 +28,19 @@ struct Dims {
   static constexpr int kTileBytes = kChunks * kChunkBytes;
 };
 
+// Whether the phase of `bar` with the given parity has completed; does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // One lane of a converged warp.  Unlike a test of the lane number it tells the compiler that the
 // code behind it is one thread's, so that the operands of TMA and MMA instructions are computed
 // in uniform registers.

@@ -380,14 +380,17 @@ pf_status pf_masked_attn_bwd(const pf_masked_attn_config* cfg, const void* dout,
   p.scale = scale_of(c);
   const int64_t row = static_cast<int64_t>(c.heads_q) * c.head_dim;
   const pf_strides whole = {row * c.n_q, row, c.head_dim};
-  CUtensorMap maps[4];
+  CUtensorMap maps[2][4];
   std::memset(maps, 0, sizeof(maps));
-  if (c.n_q > 0 && (!pf::encode_heads_map(&maps[0], q, c.batch, c.n_q, c.heads_q, c.head_dim, c.q, 1, 128) ||
-                    !pf::encode_heads_map(&maps[3], dout, c.batch, c.n_q, c.heads_q, c.head_dim, whole, 1, 128)))
-    return PF_ERR_CUDA;
-  if (c.n_k > 0 && (!pf::encode_heads_map(&maps[1], k, c.batch, c.n_k, c.heads_kv, c.head_dim, c.k, 1, 128) ||
-                    !pf::encode_heads_map(&maps[2], v, c.batch, c.n_k, c.heads_kv, c.head_dim, c.v, 1, 128)))
-    return PF_ERR_CUDA;
+  for (int box = 0; box < 2; ++box) {
+    const int rows = box == 0 ? 128 : 64;
+    auto map = [&](int which, const void* base, int n, int heads, const pf_strides& strides) {
+      return n == 0 || pf::encode_heads_map(&maps[box][which], base, c.batch, n, heads, c.head_dim, strides, 1, rows);
+    };
+    if (!map(0, q, c.n_q, c.heads_q, c.q) || !map(1, k, c.n_k, c.heads_kv, c.k) || !map(2, v, c.n_k, c.heads_kv, c.v) ||
+        !map(3, dout, c.n_q, c.heads_q, whole))
+      return PF_ERR_CUDA;
+  }
   return from_attn(pf::launch_masked_bwd(p, maps, static_cast<cudaStream_t>(stream)));
 }
 

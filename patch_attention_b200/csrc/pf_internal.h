@@ -191,8 +191,8 @@ struct MaskedBwdParams {
   int batch, heads_q, heads_kv, head_dim;
   float scale;
 };
-// maps: q, k, v, dout with boxes of one head x 128 rows.
-cudaError_t launch_masked_bwd(MaskedBwdParams& p, const CUtensorMap (&maps)[4], cudaStream_t stream);
+// maps: q, k, v, dout with boxes of one head x 128 rows [0] and x 64 rows [1].
+cudaError_t launch_masked_bwd(MaskedBwdParams& p, const CUtensorMap (&maps)[2][4], cudaStream_t stream);
 
 // Address of the current device's status word.
 cudaError_t watchdog_word(unsigned** word);
