@@ -136,18 +136,17 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
   const int part = p.n_split > 1 ? static_cast<int>(cluster_rank()) : 0;
   {
     int idx = static_cast<int>(blockIdx.x) / p.n_split;
-    int grp = idx % p.n_groups;
-    idx /= p.n_groups;
-    // the last queries of a causal mask see the most keys: they start first
-    if (mk.causal) grp = p.n_groups - 1 - grp;
     const int heads = p.pack > 1 ? p.heads_kv : p.heads_q;
+    const int grp = p.heads_first ? idx / (heads * p.batch) : idx % p.n_groups;
+    idx = p.heads_first ? idx % (heads * p.batch) : idx / p.n_groups;
     const int hd = idx % heads;
     w.b = idx / heads;
     const int share = p.heads_q / p.heads_kv;
     w.head0 = p.pack > 1 ? hd * share : hd;
     w.kv_head = p.pack > 1 ? hd : hd / share;
     w.rows_per_tile = kRows / p.pack;
-    w.q0 = grp * NQ * w.rows_per_tile;
+    // the last queries of a causal mask see the most keys: they start first
+    w.q0 = (mk.causal ? p.n_groups - 1 - grp : grp) * NQ * w.rows_per_tile;
   }
   const int prefix = mk.prefix != nullptr ? __ldg(mk.prefix + w.b) : 0;
   DocRange qdoc[NQ];
@@ -417,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
     const int* ids = mk.doc_k + static_cast<long long>(w.b) * mk.n_k;
     const float slope = MOD && mk.slopes != nullptr && in_range ? __ldg(mk.slopes + head) * kLog2e : 0.f;
     const int place = query + (mk.n_k - mk.n_q);
-    const float c = MOD ? 1.f : mk.scale_log2;
+    // scores are c s + rest in log2 units; the cap leaves them there itself
+    const float c = MOD && mk.cap_log2 > 0.f ? 1.f : mk.scale_log2;
     float m = -INFINITY;  // reference row maximum, in log2 units
     float l = 0.f;
     bool ok = true;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
       for (int h = 0; h < 2; ++h) {
         const int base = j * kRows + h * 64;
         int id0 = -1, id1 = -1;
-        if (kind == 1 && mk.doc_q != nullptr) {  // ahead of the wait
+        if (__builtin_expect(kind == 1, 0) && mk.doc_q != nullptr) {  // ahead of the wait
           if (base + lane < mk.n_k) id0 = __ldg(ids + base + lane);
           if (base + 32 + lane < mk.n_k) id1 = __ldg(ids + base + 32 + lane);
         }
@@ -444,11 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
         reg_fence<64>(s);
         float rest = 0.f;  // to be added to every score of the row
         if constexpr (MOD) {
-          if (mk.cap_log2 > 0.f) tanh_scores<64>(s, mk);
-          scale_scores<64>(s, mk.cap_log2 > 0.f ? mk.cap_log2 : mk.scale_log2);
-          if (mk.slopes != nullptr) rest = add_bias<64>(s, slope, base - place);
+          if (mk.cap_log2 > 0.f) tanh_scores<64>(s, mk, mk.cap_log2);
+          if (mk.slopes != nullptr) rest = add_bias<64>(s, slope, c, base - place);
         }
-        if (kind == 1) {
+        if (__builtin_expect(kind == 1, 0)) {
           uint64_t bits = limit_bits(limit, base);
           if (mk.doc_q != nullptr) bits &= document_bits(doc, id0, id1);
           const uint32_t lo = static_cast<uint32_t>(bits), hi = static_cast<uint32_t>(bits >> 32);
@@ -458,12 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
             if (!(hi >> k & 1u)) s[k + 32] = __float_as_uint(-INFINITY);
           }
         }
-        const float mxs = MOD ? row_max64(s) + rest : row_max64(s) * c;
+        const float mxs = MOD ? fmaf(row_max64(s), c, rest) : row_max64(s) * c;
         // O is rescaled only when the maximum grows by more than 2^8 (or is NaN): exact, as the
         // final O / l uses one reference for both
         const bool grow = in_range && !(mxs <= m + 8.f);
         const bool any_grow = __any_sync(0xffffffffu, grow);
-        if (any_grow) {
+        if (__builtin_expect(any_grow, 0)) {
           const float alpha = grow ? ex2(m - mxs) : 1.f;
           if (n > 0 || h > 0) {
             // O holds earlier PVs: this half's last one is complete (its scores are); wait for
@@ -473,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < Dm::kMmaN; c0 += 16) {
               uint32_t o[16];
               tmem_ld16(tO + c0, o);
@@ -497,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             const float2 raw = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
-            const float2 x = MOD ? __fadd2_rn(raw, nm) : __ffma2_rn(raw, cc, nm);
+            const float2 x = __ffma2_rn(raw, cc, nm);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
             acc[k & 3] = __fadd2_rn(acc[k & 3], e);
             pk[k] = pack2(e.x, e.y);  // bf16 probabilities: the MMA's operand type
@@ -710,6 +709,9 @@ void masked_fwd_plan(MaskedFwdParams& p, int n_sms) {
   }
   // two query tiles per CTA share each key tile's load
   p.n_groups = p.n_split == 1 && q_tiles > 1 && pairs > n_sms ? (q_tiles + 1) / 2 : q_tiles;
+  // The longest CTAs of a causal mask start first over all heads, so that the short ones fill the
+  // last round of SMs; head by head where the keys and values of all of them would not stay in L2.
+  p.heads_first = p.m.causal && 4.0 * p.batch * p.heads_kv * p.m.n_k * p.head_dim <= 64e6;
   p.cls_bytes = p.m.doc_q != nullptr ? (k_tiles + 15) / 16 * 16 : 0;
 }
 

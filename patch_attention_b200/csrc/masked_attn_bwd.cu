@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
         float rest = 0.f;
         if constexpr (MOD) {
           if (mk.cap_log2 > 0.f) {
-            tanh_scores<64>(s, mk);
+            tanh_scores<64>(s, mk, 1.f);
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
               const float2 t = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
             for (int k = 0; k < 32; ++k) pd[k] = both(1.f);
           }
           scale_scores<64>(s, mk.cap_log2 > 0.f ? mk.cap_log2 : mk.scale_log2);
-          if (mk.slopes != nullptr) rest = add_bias<64>(s, slope, base + (KEYS ? off - row : -off - row));
+          if (mk.slopes != nullptr) rest = add_bias<64>(s, slope, 1.f, base + (KEYS ? off - row : -off - row));
         }
         if (partly) {
           const uint32_t lo = static_cast<uint32_t>(bits), hi = static_cast<uint32_t>(bits >> 32);

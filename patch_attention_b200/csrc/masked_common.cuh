@@ -232,7 +232,7 @@ __device__ __forceinline__ void class_tiles(const int* ids, int count, int j0, i
 //         are at |e + k|; where every row of the warp lies on one side of them that is linear in
 //         k, and the row's part goes into the exponential's reference.
 // (One special-function result per element for the softmax and two for the exact tanh: they
-// bound a capped tile at 3072 cycles, the polynomial at about 1100.)
+// bound a capped tile of 128 x 128 at three times 1024 cycles, the polynomial at about 1100.)
 constexpr float kTanh0 = 0.99999768f, kTanh1 = -0.33320656f, kTanh2 = 0.13145144f, kTanh3 = -0.043372445f;
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
@@ -249,43 +249,42 @@ __device__ __forceinline__ float abs_max(const uint32_t (&s)[N]) {
   return max3_nan(mv[0], mv[1], max3_nan(mv[2], mv[3], mv[3]));
 }
 
-// Raw products to tanh(scale qk / cap), in place; the whole warp takes one way.
+// Raw products to factor tanh(scale qk / cap), in place; the whole warp takes one way.
 template <int N>
-__device__ __forceinline__ void tanh_scores(uint32_t (&s)[N], const MaskParams& m) {
+__device__ __forceinline__ void tanh_scores(uint32_t (&s)[N], const MaskParams& m, float factor) {
   const bool small = abs_max<N>(s) <= m.cap_half;
   if (__all_sync(0xffffffffu, small)) {
+    const float t0 = kTanh0 * factor, t1 = kTanh1 * factor, t2 = kTanh2 * factor, t3 = kTanh3 * factor;
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
       const float2 y = __fmul2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), both(m.cap_in));
       const float2 z = __fmul2_rn(y, y);
-      float2 p = __ffma2_rn(z, both(kTanh3), both(kTanh2));
-      p = __ffma2_rn(p, z, both(kTanh1));
-      p = __fmul2_rn(__ffma2_rn(p, z, both(kTanh0)), y);
+      float2 p = __ffma2_rn(z, both(t3), both(t2));
+      p = __ffma2_rn(p, z, both(t1));
+      p = __fmul2_rn(__ffma2_rn(p, z, both(t0)), y);
       s[k] = __float_as_uint(p.x);
       s[k + 1] = __float_as_uint(p.y);
     }
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      s[k] = __float_as_uint(fmaf(-2.f, rcp(ex2(__uint_as_float(s[k]) * (2.f * kLog2e * m.cap_in)) + 1.f), 1.f));
+      s[k] = __float_as_uint(fmaf(-2.f * factor, rcp(ex2(__uint_as_float(s[k]) * (2.f * kLog2e * m.cap_in)) + 1.f), factor));
   }
 }
 
 // Adds the bias to N scores: the columns' distances are |e + k|.  Returns what is still to be
-// added to every score of the row (0 where a row lies inside the columns).
+// added to every score of the row (0 where a row lies inside the columns), in log2 units; the
+// scores are in units of `unit` of those.
 template <int N>
-__device__ __forceinline__ float add_bias(uint32_t (&s)[N], float slope, int e) {
+__device__ __forceinline__ float add_bias(uint32_t (&s)[N], float slope_log2, float unit, int e) {
+  const float slope = slope_log2 / unit;
   const bool right = __all_sync(0xffffffffu, e >= 0), left = __all_sync(0xffffffffu, e + N - 1 <= 0);
   if (right || left) {
     const float b = right ? -slope : slope;
 #pragma unroll
-    for (int k = 0; k < N; k += 2) {
-      const float2 v = __ffma2_rn(make_float2(static_cast<float>(k), static_cast<float>(k + 1)), both(b),
-                                  make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
-      s[k] = __float_as_uint(v.x);
-      s[k + 1] = __float_as_uint(v.y);
-    }
-    return b * static_cast<float>(e);
+    for (int k = 0; k < N; ++k)  // one FMA with an immediate; on pairs the columns would be moved to registers first
+      s[k] = __float_as_uint(fmaf(b, static_cast<float>(k), __uint_as_float(s[k])));
+    return (right ? -slope_log2 : slope_log2) * static_cast<float>(e);
   }
 #pragma unroll
   for (int k = 0; k < N; ++k)

@@ -170,6 +170,7 @@ struct MaskedFwdParams {
   int pack;       // query heads of one key head that share a tile (1: one head per tile)
   int n_groups;   // query-tile groups per head (block)
   int n_split;    // CTAs (a cluster) that share a query tile's keys
+  int heads_first;  // grid order: the heads of a query-tile group are neighbours (else its groups)
   int cls_bytes;  // shared bytes for the documents' tile classes
 };
 constexpr int kMaskedDocTiles = 8192;  // key tiles that a call with documents may have
