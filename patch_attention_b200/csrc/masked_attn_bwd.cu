@@ -29,6 +29,7 @@
 // Streaming rows whose product with a zero probability must not be NaN -- queries that see nothing
 // (lse = -inf), keys that no query of the tile sees -- are zeroed in shared memory first.
 
+#include <algorithm>
 #include <mutex>
 
 #include "masked_common.cuh"
@@ -92,10 +93,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
   const int x_tiles = ((KEYS ? mk.n_k : mk.n_q) + kRows - 1) / kRows;
   const int y_tiles = ((KEYS ? mk.n_q : mk.n_k) + kRows - 1) / kRows;
   int idx = static_cast<int>(blockIdx.x);
-  int xt = idx % x_tiles;
-  idx /= x_tiles;
-  if (!KEYS && mk.causal) xt = x_tiles - 1 - xt;  // the last queries see the most keys: they start first
   const int heads = KEYS ? p.heads_kv : p.heads_q;
+  int xt = p.heads_first ? idx / (heads * p.batch) : idx % x_tiles;
+  idx = p.heads_first ? idx % (heads * p.batch) : idx / x_tiles;
+  if (!KEYS && mk.causal) xt = x_tiles - 1 - xt;  // the last queries see the most keys: they start first
   const int x_head = idx % heads;
   const int b = idx / heads;
   const int rounds = KEYS ? share : 1;  // query heads that stream past
@@ -149,6 +150,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (KEYS) {
+    // delta comes from the grid before this one.  With it complete the grid of the queries may
+    // start where this one leaves SMs idle: they have no results in common.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
 
   // how this CTA's rows and streaming tile j see each other: 0 not at all, 1 in part, 2 entirely
   auto see = [&](int j) {
@@ -607,6 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  // what follows in the stream waits for this grid alone: it ends after the keys' grid
+  if (!KEYS && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // delta[b][h][i] = sum_d o do, one head vector per LANES lanes of 8 elements each.
@@ -635,7 +644,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const uint4* __restrict__ o,
 }
 
 template <int D, bool KEYS, bool MOD>
-cudaError_t launch(const MaskedBwdParams& p, cudaStream_t stream) {
+cudaError_t launch(const MaskedBwdParams& p, bool overlap, cudaStream_t stream) {
   static std::mutex mu;
   static uint64_t done = 0;  // bit per device ordinal
   constexpr int kMaxSmem = smem_bytes<D>(kMaskedDocTiles);
@@ -657,12 +666,24 @@ cudaError_t launch(const MaskedBwdParams& p, cudaStream_t stream) {
   const int y_tiles = ((KEYS ? p.m.n_q : p.m.n_k) + kRows - 1) / kRows;
   const unsigned grid = static_cast<unsigned>(p.batch) * (KEYS ? p.heads_kv : p.heads_q) * x_tiles;
   if (grid == 0) return cudaSuccess;
-  kernel<<<grid, kThreads, smem_bytes<D>(p.m.doc_q != nullptr ? (y_tiles + 15) / 16 * 16 : 0), stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<D>(p.m.doc_q != nullptr ? (y_tiles + 15) / 16 * 16 : 0);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int D, bool MOD>
 cudaError_t launch_dim(MaskedBwdParams& p, const CUtensorMap (&maps)[2][4], cudaStream_t stream) {
+  // the longest CTAs of a causal mask first over all heads, while their streaming tensors stay in L2
+  const double rows = std::max(static_cast<double>(p.heads_q) * p.m.n_q, static_cast<double>(p.heads_kv) * p.m.n_k);
+  p.heads_first = p.m.causal && 4.0 * p.batch * D * rows <= 64e6;
   const long long vectors = static_cast<long long>(p.batch) * p.m.n_q * p.heads_q;
   if (vectors > 0) {
     const long long blocks = (vectors * (D <= 64 ? 8 : 16) + 255) / 256;
@@ -675,13 +696,16 @@ cudaError_t launch_dim(MaskedBwdParams& p, const CUtensorMap (&maps)[2][4], cuda
   p.tm_x2 = maps[0][2];
   p.tm_y1 = maps[1][0];
   p.tm_y2 = maps[1][3];
-  const cudaError_t e = launch<D, true, MOD>(p, stream);
+  // each starts under the one before: dK, dV's prologue under delta's end, dQ in the SMs that dK, dV
+  // leaves idle (see the kernel for what they wait for)
+  const bool overlap = p.m.n_k > 0 && vectors > 0;
+  const cudaError_t e = launch<D, true, MOD>(p, overlap, stream);
   if (e != cudaSuccess) return e;
   p.tm_x1 = maps[0][0];  // Q, dO stay; K, V stream
   p.tm_x2 = maps[0][3];
   p.tm_y1 = maps[1][1];
   p.tm_y2 = maps[1][2];
-  return launch<D, false, MOD>(p, stream);
+  return launch<D, false, MOD>(p, overlap, stream);
 }
 
 }  // namespace

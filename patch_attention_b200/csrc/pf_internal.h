@@ -190,6 +190,7 @@ struct MaskedBwdParams {
   unsigned* watchdog;
   MaskParams m;
   int batch, heads_q, heads_kv, head_dim;
+  int heads_first;  // grid order, as in the forward kernel
   float scale;
 };
 // maps: q, k, v, dout with boxes of one head x 128 rows [0] and x 64 rows [1].
