@@ -161,6 +161,16 @@ __device__ __forceinline__ void stage_params(float* to, const void* base, long l
     }
   }
 }
+// A group's 16-bit parameters in shared memory, in order; 0 where there are none.
+template <typename T, int VEC>
+__device__ __forceinline__ void copy_params(T* to, const void* base, long long row, int channels) {
+#pragma unroll 2
+  for (int c = threadIdx.x * VEC; c < channels; c += blockDim.x * VEC) {
+    Unit<T, VEC> v = {};
+    if (base != nullptr) v = load_vec<T, VEC>(static_cast<const T*>(base) + row + c);
+    *reinterpret_cast<Unit<T, VEC>*>(to + c) = v;
+  }
+}
 template <int VEC, int N>
 __device__ __forceinline__ void staged_params(float2 (&f)[N], const float* from, int k, int lane, const Place<VEC>& at,
                                               int n) {
@@ -193,25 +203,25 @@ struct Exchange {
 // KIND 0: a warp takes one row, parameters from global memory (few rows: least latency).
 // KIND 1: a block of four warps walks rows of one group, its parameters in shared memory.
 // KIND 2: a block of up to 16 warps takes one row.
+// KIND 3: as 1, with 16-bit parameters left as they are in shared memory: as fp32 their reads were
+//         most of the time of a bf16 row (2 x 16384 x 1536 modulated: 39 us, 70% of L1's rate).
 template <typename T, int VEC, int EPT, int KIND>
 __global__ void __launch_bounds__(KIND == 2 ? 512 : 128) ln_fwd_kernel(const __grid_constant__ LnParams p) {
   using Wk = Walk<VEC, EPT>;
-  constexpr bool WIDE = KIND == 2;
+  constexpr bool WIDE = KIND == 2, WALK = KIND == 1 || KIND == 3;
   __shared__ float2 slots[2][16];
-  __shared__ __align__(16) float staged[KIND == 1 ? 2 * 32 * EPT : 4];
+  __shared__ __align__(16) float staged[KIND == 1 ? 2 * 32 * EPT : KIND == 3 ? 32 * EPT : 4];
+  T* narrow = reinterpret_cast<T*>(staged);  // KIND 3: weights, then biases
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = p.channels;
   long long row, end, g;
   int step = 1;
-  if constexpr (KIND == 1) {
+  if constexpr (WALK) {
     g = blockIdx.x / p.parts;
     const int part = static_cast<int>(blockIdx.x % p.parts);
     row = g * p.rows_per_group + p.rows_per_group * part / p.parts + warp;
     end = g * p.rows_per_group + p.rows_per_group * (part + 1) / p.parts;
     step = 4;
-    stage_params<T, VEC>(staged, p.weight, g * p.weight_stride, p.w0, 1.f, p);
-    stage_params<T, VEC>(staged + 32 * EPT, p.bias, g * p.bias_stride, 0.f, 0.f, p);
-    __syncthreads();
   } else {
     row = KIND == 2 ? blockIdx.x : static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
     if (row >= p.rows) return;
@@ -222,7 +232,7 @@ __global__ void __launch_bounds__(KIND == 2 ? 512 : 128) ln_fwd_kernel(const __g
   const float mine = static_cast<float>(min(max(n - first, 0), 32 * EPT));
   const float inv_mine = mine > 0.f ? 1.f / mine : 0.f, inv_n = 1.f / static_cast<float>(n);
   const Place<VEC> at = {first + lane * VEC};
-  if (KIND == 1 && row >= end) return;
+  const float plus = p.weight != nullptr ? p.w0 : 1.f;
   Unit<T, VEC> raw[EPT / VEC];
   auto fetch = [&](long long r) {
     const T* x = static_cast<const T*>(p.x) + r * n;
@@ -230,7 +240,17 @@ __global__ void __launch_bounds__(KIND == 2 ? 512 : 128) ln_fwd_kernel(const __g
     for (int i = 0; i < EPT / VEC; ++i)
       if (Wk::template in<WIDE>(i, at, n)) raw[i] = load_vec<T, VEC>(x + at.column(i));
   };
-  fetch(row);
+  if (row < end) fetch(row);
+  if constexpr (WALK) {
+    if constexpr (KIND == 1) {
+      stage_params<T, VEC>(staged, p.weight, g * p.weight_stride, p.w0, 1.f, p);
+      stage_params<T, VEC>(staged + 32 * EPT, p.bias, g * p.bias_stride, 0.f, 0.f, p);
+    } else {
+      copy_params<T, VEC>(narrow, p.weight, g * p.weight_stride, p.channels);
+      copy_params<T, VEC>(narrow + 32 * EPT, p.bias, g * p.bias_stride, p.channels);
+    }
+    __syncthreads();
+  }
   for (; row < end; row += step) {
     float2 f[EPT / 2];
     float2 s2 = both(0.f);
@@ -248,7 +268,7 @@ __global__ void __launch_bounds__(KIND == 2 ? 512 : 128) ln_fwd_kernel(const __g
         }
       }
     }
-    if (KIND == 1 && row + step < end) fetch(row + step);  // while this row is reduced
+    if (WALK && row + step < end) fetch(row + step);  // while this row is reduced
     float mean = warp_sum(s2.x + s2.y) * inv_mine;
     float2 q2 = both(0.f);
 #pragma unroll
@@ -293,6 +313,14 @@ __global__ void __launch_bounds__(KIND == 2 ? 512 : 128) ln_fwd_kernel(const __g
       if constexpr (KIND == 1) {
         staged_params<VEC>(w, staged, k, lane, at, n);
         staged_params<VEC>(b, staged + 32 * EPT, k, lane, at, n);
+      } else if constexpr (KIND == 3) {
+        const Unit<T, VEC> wv = *reinterpret_cast<const Unit<T, VEC>*>(narrow + at.column(k));
+        const Unit<T, VEC> bv = *reinterpret_cast<const Unit<T, VEC>*>(narrow + 32 * EPT + at.column(k));
+#pragma unroll
+        for (int u = 0; u < Wk::P; ++u) {
+          w[u] = add2(pair_of<T>(wv.v + 2 * u), both(plus));
+          b[u] = pair_of<T>(bv.v + 2 * u);
+        }
       } else {
         direct_params<T, VEC>(w, p.weight, g * p.weight_stride, p.w0, 1.f, k, p, at);
         direct_params<T, VEC>(b, p.bias, g * p.bias_stride, 0.f, 0.f, k, p, at);
@@ -592,11 +620,18 @@ cudaError_t launch_cut(LnParams& p, long long groups, bool bwd, cudaStream_t str
     ln_bwd_kernel<T, VEC, EPT, WIDE><<<static_cast<unsigned>(groups * p.parts), threads, smem, stream>>>(p);
     return cudaGetLastError();
   }
-  if (!WIDE && p.rows >= kSms * kFwdBlocks * 4 * 4 && p.rows_per_group >= 16) {
-    // at least four rows for each warp that is resident, and for each warp of a group
-    const long long parts = kSms * kFwdBlocks / groups, most = p.rows_per_group / 16;
+  if (!WIDE && p.rows >= kSms * kFwdBlocks * 8 && p.rows_per_group >= 16) {
+    // As many blocks as are resident, or four times that where each of them would still have eight
+    // rows: short blocks even out the SMs' different speeds (2 x 16384 x 1536: 43.8 us in one round,
+    // 38.5 in four), long ones read the parameters less often (4 x 4096 x 1152: 15.9 and 17.3 us).
+    const long long rounds = p.rows >= kSms * kFwdBlocks * 32 ? 4 : 1;
+    const long long parts = kSms * kFwdBlocks * rounds / groups, most = p.rows_per_group / 16;
     p.parts = static_cast<int>(parts < 1 ? 1 : parts < most ? parts : most);
-    ln_fwd_kernel<T, VEC, EPT, WIDE ? 2 : 1><<<static_cast<unsigned>(groups * p.parts), 128, 0, stream>>>(p);
+    const unsigned grid = static_cast<unsigned>(groups * p.parts);
+    if (VEC == 8 && !p.wide)
+      ln_fwd_kernel<T, VEC, EPT, WIDE ? 2 : VEC == 8 ? 3 : 1><<<grid, 128, 0, stream>>>(p);
+    else
+      ln_fwd_kernel<T, VEC, EPT, WIDE ? 2 : 1><<<grid, 128, 0, stream>>>(p);
     return cudaGetLastError();
   }
   // one warp per block while that still leaves SMs without work, else four
