@@ -405,6 +405,13 @@ ln_bwd_kernel(const __grid_constant__ LnParams p) {
   float2 aw[EPT / 2], ab[EPT / 2];
 #pragma unroll
   for (int k = 0; k < EPT / 2; ++k) aw[k] = ab[k] = both(0.f);
+  long long row = lo + (WIDE ? 0 : warp);
+  float mean = 0.f, rstd = 0.f;
+  if (row < hi) {
+    fetch(row, 0);
+    mean = p.mean[row];
+    rstd = p.rstd[row];
+  }
   if constexpr (!WIDE) {
     stage_params<T, VEC>(staged, p.weight, g * p.weight_stride, p.w0, 1.f, p);
     __syncthreads();
@@ -415,10 +422,7 @@ ln_bwd_kernel(const __grid_constant__ LnParams p) {
     else
       staged_params<VEC>(w, staged, k, lane, at, n);
   };
-  long long row = lo + (WIDE ? 0 : warp);
   if (row < hi) {
-    fetch(row, 0);
-    float mean = p.mean[row], rstd = p.rstd[row];
     const int flip = p.stages - 1;
     for (int stage = 0;; stage ^= flip) {
       const bool more = row + kStep < hi;
