@@ -227,7 +227,7 @@ __device__ __forceinline__ void load_gain(const void* g, const Lane& ln, float2 
 
 // FULL: every pair turns.
 template <typename T, bool INTER, int PV, int SEG, bool FULL>
-__global__ void __launch_bounds__(32 * kWarps) rope_fwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * kWarps, INTER ? 7 : 0) rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPer = 32 / SEG;
   constexpr int kSteps = 4;
   __shared__ float2 cs[kWarps * 128];
@@ -235,6 +235,25 @@ __global__ void __launch_bounds__(32 * kWarps) rope_fwd_kernel(const __grid_cons
   const Item it(p, blockIdx.x * static_cast<unsigned>(kWarps / p.shares), threadIdx.x >> 5, blockIdx.y, gridDim.y);
   const float inv_d = 1.f / static_cast<float>(p.head_dim);
   const bool norm = p.eps > 0.f;
+  // kSteps vectors of x, of which this lane has `left`
+  Raw<T, INTER, PV> raw[kSteps];
+  auto fetch = [&](const T*& x, long long step, int left) {
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      raw[u].zero();
+      if (u * kPer < left) raw[u].load(x, ln.e0, ln.e1);
+      x += step;
+    }
+  };
+  // Pairs of neighbours: the first vectors are on their way while the angles are computed (4096 x 24
+  // x 128: 27.7 to 25.8 us; the pieces of split halves need too many registers for that: 44.7 and
+  // 48.7 us at 16384 x 24 x 64).
+  const int w0 = !INTER ? 2 : it.lo[0] < it.hi[0] ? 0 : 1;
+  if (INTER && it.lo[w0 & 1] < it.hi[w0 & 1]) {
+    long long xstep;
+    const T* x = it.start<T, kPer>(p.x[w0 & 1], p.xs[w0 & 1], w0 & 1, ln, xstep);
+    fetch(x, xstep, ln.active ? it.hi[w0 & 1] - it.lo[w0 & 1] - ln.sub : 0);
+  }
   it.fill_angles(p, cs);
   __syncthreads();
   float2 c[2], s[2];
@@ -246,17 +265,14 @@ __global__ void __launch_bounds__(32 * kWarps) rope_fwd_kernel(const __grid_cons
     load_gain<T, INTER, PV>(p.gain[w], ln, ga, gb);
     long long xstep, ystep;
     const T* x = it.start<T, kPer>(p.x[w], p.xs[w], w, ln, xstep);
+    bool here = INTER && w == w0;  // the first vectors
+    if (here) x += kSteps * xstep;
     T* y = it.start<T, kPer>(p.y[w], p.ys[w], w, ln, ystep);
     // vectors of this lane left (none for a lane past the vector's end)
     int left = ln.active ? it.hi[w] - it.lo[w] - ln.sub : 0;
     for (int steps = (it.hi[w] - it.lo[w] + kPer - 1) / kPer; steps > 0; steps -= kSteps) {
-      Raw<T, INTER, PV> raw[kSteps];
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        raw[u].zero();
-        if (u * kPer < left) raw[u].load(x, ln.e0, ln.e1);
-        x += xstep;
-      }
+      if (!here) fetch(x, xstep, left);
+      here = false;
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
         if (u >= steps) break;  // the whole warp
