@@ -18,6 +18,15 @@
 // keys are split over a cluster of up to 8 CTAs that merge their (O, m, l) through distributed
 // shared memory -- no workspace, no counters, and the same order of sums every time.
 //
+// What bounds it, measured on a B200: at head_dim 128 the tensor core (24 heads x 16538 x 16538:
+// 2.62 ms, 1280 TFLOP/s); at head_dim 64 the softmax warps, two per scheduler in step with each
+// other -- of 1600 cycles per 128 x 128 tile 1024 are the special-function unit's, the rest is the
+// maximum, the TMEM copies and the hand-over (2.30 ms, 730 TFLOP/s; three packed documents 1.17 ms).
+// A cap adds 1000 cycles per tile and a bias 800 (2 x 16 x 4216, head_dim 72, causal: 145 us without,
+// 270 us with cap, bias and prefix).  Documents that end inside tiles cost the query tiles that meet
+// two of them the keys of both.  One token against 8 x 16538 keys (24 / 8 heads of 128): 108 us,
+// 5.0 TB/s of K and V.
+//
 // A value row that no query of the CTA sees may hold anything (padding, unwritten cache rows):
 // its products with the zero probabilities would still be NaN, so a warp zeroes such rows in
 // shared memory before the MMA reads them.
@@ -710,8 +719,10 @@ void masked_fwd_plan(MaskedFwdParams& p, int n_sms) {
   // two query tiles per CTA share each key tile's load
   p.n_groups = p.n_split == 1 && q_tiles > 1 && pairs > n_sms ? (q_tiles + 1) / 2 : q_tiles;
   // The longest CTAs of a causal mask start first over all heads, so that the short ones fill the
-  // last round of SMs; head by head where the keys and values of all of them would not stay in L2.
-  p.heads_first = p.m.causal && 4.0 * p.batch * p.heads_kv * p.m.n_k * p.head_dim <= 64e6;
+  // last round of SMs (2 x 16 heads x 4216 of 72: 144 us, head by head 173; 24 x 16538 of 64: 1167
+  // and 1264), while the keys and values of all heads fit in L2 (101 MB there; with 203 MB the two
+  // are even, with 4 x 24 x 8269 of 128, 406 MB, they take 1695 and 1538 us).
+  p.heads_first = p.m.causal && 4.0 * p.batch * p.heads_kv * p.m.n_k * p.head_dim <= 120e6;
   p.cls_bytes = p.m.doc_q != nullptr ? (k_tiles + 15) / 16 * 16 : 0;
 }
 
