@@ -688,8 +688,8 @@ cudaError_t launch(const MaskedBwdParams& p, bool overlap, cudaStream_t stream) 
 
 template <int D, bool MOD>
 cudaError_t launch_dim(MaskedBwdParams& p, const CUtensorMap (&maps)[2][4], cudaStream_t stream) {
-  // The longest CTAs of a causal mask first over all heads while a side's two tensors, twice what the
-  // forward pass streams, stay in L2 (2 x 16 x 1100 of 72, 10 MB: 78 us, head by head 88; 39 MB: even;
+  // The longest CTAs of a causal mask first over all heads while two tensors of the longer side take
+  // less than half of L2, beside the other side's (2 x 16 x 1100 of 72, 10 MB: 78 us, head by head 88; 39 MB: even;
   // 24 x 16538 of 64, 101 MB: 4.05 and 3.88 ms)
   const double rows = std::max(static_cast<double>(p.heads_q) * p.m.n_q, static_cast<double>(p.heads_kv) * p.m.n_k);
   p.heads_first = p.m.causal && 4.0 * p.batch * D * rows <= 64e6;
