@@ -158,6 +158,7 @@ pf_status make_mask(const pf_masked_attn_config& c, const float* slopes, const i
   if ((doc_q != nullptr) != (doc_k != nullptr) && c.n_q > 0 && c.n_k > 0) return PF_ERR_INVALID_ARG;
   const bool docs = doc_q && doc_k;
   if (docs && c.n_k > pf::kMaskedDocTiles * 128) return PF_ERR_SHAPE;
+  if (slopes && scale_of(c) < 1e-20f) return PF_ERR_INVALID_ARG;  // the forward kernel divides them by the scale
   if (!aligned(slopes, 4) || !aligned(prefix, 4) || !aligned(doc_q, 4) || !aligned(doc_k, 4)) return PF_ERR_ALIGN;
   m.prefix = prefix;
   m.doc_q = docs ? doc_q : nullptr;

@@ -216,3 +216,11 @@ def test_python_refuses_cpu_tensors_and_bad_layouts():
         pa.RopeAxes((2, 2, 2, 2, 2))
     with pytest.raises(ValueError):
         pa.RopeAxes((2, 2), theta=(1.0,))
+
+
+def test_bias_needs_a_scale_to_divide_by():
+    slopes = FAKE
+    for scale, status in ((1e-21, pa.PF_ERR_INVALID_ARG), (1e-30, pa.PF_ERR_INVALID_ARG)):
+        cfg = _attn_cfg(softmax_scale=scale)
+        assert _attn(cfg, slopes=slopes) == status
+        assert _attn_bwd(cfg, slopes=slopes) == status
