@@ -631,8 +631,8 @@ cudaError_t launch_cut(LnParams& p, long long groups, bool bwd, cudaStream_t str
     return cudaGetLastError();
   }
   if (!WIDE && p.rows >= kSms * kFwdBlocks * 8 && p.rows_per_group >= 16) {
-    // As many blocks as are resident, or four times that where each of them would still have eight
-    // rows: short blocks even out the SMs' different speeds (2 x 16384 x 1536: 43.8 us in one round,
+    // As many blocks as are resident, or up to four times that, of sixteen rows at least: short
+    // blocks even out the SMs' different speeds (2 x 16384 x 1536: 43.8 us in one round,
     // 38.5 in four), long ones read the parameters less often (4 x 4096 x 1152: 15.9 and 17.3 us).
     const long long rounds = p.rows >= kSms * kFwdBlocks * 32 ? 4 : 1;
     const long long parts = kSms * kFwdBlocks * rounds / groups, most = p.rows_per_group / 16;

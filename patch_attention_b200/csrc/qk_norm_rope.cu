@@ -17,8 +17,8 @@
 // positions lose nothing.
 // Measured on a B200: 4096 x (24 + 24) x 128 bf16 forward 25.5 us, 4.0 TB/s, backward 51 us; 16384 x
 // (24 + 24) x 64 forward 42 us (neighbouring pairs) and 44 us (split halves), 4.6 to 4.8 TB/s,
-// backward 82 and 105 us.  What is left of HBM's rate goes to the start of each block (its angles),
-// and in the backward pass to the registers of two tensors' vectors and the gains' sums.
+// backward 82 and 105 us.  What is left of HBM's rate goes to the start of each block (its angles)
+// and to instruction issue (61% of the slots), and in the backward pass to the registers of two tensors' vectors and the gains' sums.
 //
 // The backward pass keeps the gain-gradient sums of a lane's elements in registers while its
 // block walks tokens; blocks write fp32 partials that a second kernel adds in a fixed order.
