@@ -381,7 +381,8 @@ ln_bwd_kernel(const __grid_constant__ LnParams p) {
   float* staged = reinterpret_cast<float*>(shared);
   uint8_t* dyn = shared + (WIDE ? 0 : 32 * EPT * sizeof(float));
   __shared__ float2 slots[2][16];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // only for the reduction: other programmatic dependents may read their inputs as soon as they start
+  if (p.part != nullptr) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Exchange ex{slots};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = p.channels;

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_bwd_kernel(const __grid_co
     // delta comes from the grid before this one.  With it complete the grid of the queries may
     // start where this one leaves SMs idle: they have no results in common.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.overlap) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
 
   // how this CTA's rows and streaming tile j see each other: 0 not at all, 1 in part, 2 entirely
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const uint4* __restrict__ o,
 }
 
 template <int D, bool KEYS, bool MOD>
-cudaError_t launch(const MaskedBwdParams& p, bool overlap, cudaStream_t stream) {
+cudaError_t launch(const MaskedBwdParams& p, cudaStream_t stream) {
   static std::mutex mu;
   static uint64_t done = 0;  // bit per device ordinal
   constexpr int kMaxSmem = smem_bytes<D>(kMaskedDocTiles);
@@ -682,7 +682,7 @@ cudaError_t launch(const MaskedBwdParams& p, bool overlap, cudaStream_t stream) 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = overlap ? 1 : 0;
+  cfg.numAttrs = p.overlap ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -707,14 +707,14 @@ cudaError_t launch_dim(MaskedBwdParams& p, const CUtensorMap (&maps)[2][4], cuda
   p.tm_y2 = maps[1][3];
   // each starts under the one before: dK, dV's prologue under delta's end, dQ in the SMs that dK, dV
   // leaves idle (see the kernel for what they wait for)
-  const bool overlap = p.m.n_k > 0 && vectors > 0;
-  const cudaError_t e = launch<D, true, MOD>(p, overlap, stream);
+  p.overlap = p.m.n_k > 0 && vectors > 0;
+  const cudaError_t e = launch<D, true, MOD>(p, stream);
   if (e != cudaSuccess) return e;
   p.tm_x1 = maps[0][0];  // Q, dO stay; K, V stream
   p.tm_x2 = maps[0][3];
   p.tm_y1 = maps[1][1];
   p.tm_y2 = maps[1][2];
-  return launch<D, false, MOD>(p, overlap, stream);
+  return launch<D, false, MOD>(p, stream);
 }
 
 }  // namespace

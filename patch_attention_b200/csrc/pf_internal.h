@@ -191,6 +191,7 @@ struct MaskedBwdParams {
   MaskParams m;
   int batch, heads_q, heads_kv, head_dim;
   int heads_first;  // grid order, as in the forward kernel
+  int overlap;      // the grids of delta, of dK and dV, and of dQ overlap (all of them are launched)
   float scale;
 };
 // maps: q, k, v, dout with boxes of one head x 128 rows [0] and x 64 rows [1].

@@ -312,7 +312,8 @@ template <typename T, bool INTER, int PV, int SEG, bool FULL>
 __global__ void __launch_bounds__(32 * kWarps, 4) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPer = 32 / SEG;
   constexpr int kSteps = 2;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // only for the reduction: other programmatic dependents may read their inputs as soon as they start
+  if (p.part != nullptr) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ float2 cs[2][kWarps * 128];
   __shared__ float red[2][256];
   const Lane ln = Lane::make<INTER, SEG>(p);

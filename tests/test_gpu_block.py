@@ -242,3 +242,42 @@ def test_two_graphs_and_two_streams_at_once():
     for o, w in zip(outs, want):
         for n in w:
             assert torch.equal(o[n], w[n]), n
+
+
+def test_gradients_right_before_the_patch_attention():
+    """The patch attention reads its inputs as soon as it may start.  A backward call without parameter gradients
+    launches no second kernel, and with none to give way to it must hold the patch call back until its end."""
+    rows, c = 400_000, 256
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, dy = (torch.randn(rows, c, device="cuda", generator=g).to(BF) for _ in range(2))
+    mean, rstd = torch.zeros(2, rows, device="cuda").unbind()
+    rstd += 1
+    dx = torch.empty_like(x)
+    pos = torch.arange(rows, device="cuda", dtype=torch.float32)[:, None]
+    axes = pa.RopeAxes((64,))
+    heads = x.view(1, rows, 4, 64)
+    pat = pa.PatchAttention(1, 4, 64, 1024, 4, 0, 1)
+    whole = x[:1024].view(1, 1024, 4, 64)
+    try:
+        for kind in ("norm", "rope"):
+            outs = []
+            for wait in (True, False, False, False):
+                pat.init_layer(0, whole, whole)
+                dx.zero_()
+                torch.cuda.synchronize()
+                if kind == "norm":
+                    pa.pf_layernorm_bwd(dy, x, None, 1.0, mean, rstd, dx, None, None, None)
+                else:
+                    pa.pf_qk_norm_rope_bwd(dy.view(heads.shape), None, heads, None, pos, axes, dx.view(heads.shape), None,
+                                           None, None, 1e-6, None, None, None)
+                last = dx[-256:].view(1, 256, 4, 64)
+                if wait:
+                    torch.cuda.synchronize()
+                outs.append(pat.step(0, 0, last, last, last).clone())
+                torch.cuda.synchronize()
+                pat.check()
+            assert outs[0].any()
+            for o in outs[1:]:
+                assert torch.equal(o, outs[0]), kind
+    finally:
+        pat.close()
