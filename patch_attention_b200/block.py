@@ -381,12 +381,17 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torc
     lead = q if q is not None else k
     if lead is None:
         raise ValueError("q or k is needed")
-    i = _index(lead)
+    i = _index(lead, k, pos, gain_q, gain_k)
     if _elsewhere(i, stream):
         with _on(i, stream):
             return qk_norm_rope(q, k, pos, axes, gain_q=gain_q, gain_k=gain_k, eps=eps)
     q_out, k_out = _new(q), _new(k)
-    pf_qk_norm_rope(q, k, pos, axes, q_out, k_out, gain_q, gain_k, eps)
+    # outputs made here need no look at their layout
+    key = (axes._key, eps, _layout(q), _layout(k), _layout(pos))
+    p = _kept(_rope_plans, key, lambda: _RopePlan(q, k, pos, axes, eps, q_out, k_out, None, None))
+    gq, gk = _whole(gain_q, lead.dtype, p.gain_shape, "gain_q"), _whole(gain_k, lead.dtype, p.gain_shape, "gain_k")
+    _check(_lib().pf_qk_norm_rope(p.cfg, pos.data_ptr(), _ptr(q), p.q, _ptr(k), p.k, gq, gk, _ptr(q_out), p.q_out,
+                                  _ptr(k_out), p.k_out, _raw_stream(i)), "pf_qk_norm_rope")
     return q_out, k_out
 
 
@@ -490,15 +495,16 @@ def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rule: Op
     """Attention of bf16 q [batch, n_q, heads_q, d] over k, v [batch, n_k, heads_kv, d] (views with contiguous head
     vectors are fine; heads_q a multiple of heads_kv; d in 64, 72, 128) with the scores changed and masked by
     ``rule``.  Returns o, or (o, lse) with the fp32 [batch, heads_q, n_q] statistics of the backward pass."""
-    i = _index(q)
+    r = rule or _PLAIN
+    i = _index(q, k, v, r.slopes, r.prefix, r.doc_q, r.doc_k)
     if _elsewhere(i, stream):
         with _on(i, stream):
             return masked_attention(q, k, v, rule, want_lse=want_lse)
+    plan = _masked_plan(q, k, v, r)
     o = _new(q)
-    lse = None
-    if want_lse:
-        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=_F32, device=q.device)
-    pf_masked_attn(q, k, v, o, lse, rule)
+    lse = torch.empty(plan[1], dtype=_F32, device=q.device) if want_lse else None
+    _check(_lib().pf_masked_attn(plan[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), *_rule_ptrs(r, plan), o.data_ptr(),
+                                 _ptr(lse), _raw_stream(i)), "pf_masked_attn")
     return (o, lse) if want_lse else o
 
 
