@@ -11,6 +11,11 @@ few per cent; 1.5 of the second chain's norm is allowed.  One token's row, 64 el
 error there plus the tensor's mean row error: a row's norm spreads by 1 / sqrt(2 * 64) = 9%, and rows whose leading
 roundings cancel are covered by the mean.
 """
+import os
+import subprocess
+import sys
+import threading
+
 import pytest
 import torch
 
@@ -281,3 +286,50 @@ def test_gradients_right_before_the_patch_attention():
                 assert torch.equal(o, outs[0]), kind
     finally:
         pat.close()
+
+
+FIRST_CALLS = """
+import torch
+from tests.test_gpu_block import _params, _pos, _rule, _run
+p, pos, rule = _params(7), _pos(), _rule("documents")
+torch.cuda.synchronize()
+torch.randn(8, 8, device="cuda") @ torch.randn(8, 8, device="cuda")  # torch's own library is not what is looked at
+p["x"][0] @ p["w"], p["x"][0].t() @ p["x"][0], p["x"] @ p["w"]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = _run(p, pos, rule)
+graph.replay()
+torch.cuda.synchronize()
+want = _run(p, pos, rule)
+assert all(torch.equal(out[n], want[n]) for n in want)
+print("equal")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "equal" in r.stdout, r.stderr[-2000:]
+
+
+def test_four_host_threads_with_a_stream_each():
+    pos, rule = _pos(), _rule("documents")
+    ps = [_params(8 + i) for i in range(4)]
+    want = [_run(p, pos, rule) for p in ps]
+    torch.cuda.synchronize()
+    same = {}
+
+    def go(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = _run(ps[i], pos, rule)
+            stream.synchronize()
+            same[i] = all(torch.equal(got[n], want[i][n]) for n in got)
+
+    threads = [threading.Thread(target=go, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert same == {0: True, 1: True, 2: True, 3: True}
