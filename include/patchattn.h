@@ -280,7 +280,7 @@ typedef struct {
 
 /*   q, k, v : device bf16, [batch, n_q, heads_q, d] and [batch, n_k, heads_kv, d] by their strides
  *   slopes  : device fp32 [heads_q] or NULL, below 1e15 in size; softmax_scale is then at least 1e-20
- *   prefix  : device int32 [batch] or NULL; only with causal
+ *   prefix  : device int32 [batch] or NULL; only with causal; zero and below: no prefix
  *   doc_q, doc_k : device int32 [batch, n_q], [batch, n_k], contiguous, or both NULL
  *   o       : device bf16 [batch, n_q, heads_q, d] contiguous, not overlapping an input
  *   lse     : device fp32 [batch, heads_q, n_q] or NULL: log of the sum of exp(s) over the visible

@@ -114,12 +114,13 @@ __device__ __forceinline__ bool named_bar_and(int id, int count, bool pred) {
 // ------------------------------------------------------------------ masks
 
 // The last key that a query row may see by position (its own position under the causal mask,
-// or the prefix where that reaches further); -1: none.  Rows stand at query + n_k - n_q.
+// or the prefix where that reaches further; a prefix below zero is none); -1: no key.  Rows stand
+// at query + n_k - n_q.
 __device__ __forceinline__ int key_limit(const MaskParams& m, int query, int prefix) {
   const int last = m.n_k - 1;
   if (!m.causal) return last;
   const int at = query + (m.n_k - m.n_q);
-  return max(min(max(at, prefix - 1), last), -1);
+  return max(min(max(at, max(prefix, 0) - 1), last), -1);
 }
 
 // Bit k set: key base + k is at most `limit` (64 keys).
