@@ -604,8 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
             acc[k] = ld_cluster4(a + c * 4);
           }
         }
+        // a part whose row is NaN (a NaN or infinite score) makes the whole row NaN, as in one part
 #pragma unroll
-        for (int k = 0; k < kMaxSplit; ++k) top = fmaxf(top, ml[k].x);
+        for (int k = 0; k < kMaxSplit; ++k) top = max3_nan(top, ml[k].x, ml[k].x);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         float l = 0.f;
         if (top != -INFINITY) {

@@ -34,3 +34,43 @@ def test_a_prefix_below_zero_is_none(prefix, nq, nk, d):
     first = [t[:1].contiguous() for t in (q, k, v)]
     got = forward_and_backward(*first, pa.ScoreRule(causal=True, prefix=p[:1].contiguous()))
     assert same(got, forward_and_backward(*first, pa.ScoreRule(causal=True)))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("hq,hk,d", [(1, 1, 64), (2, 2, 72), (6, 2, 128)])
+def test_a_nan_or_infinite_score_shows_where_keys_are_split(value, hq, hk, d):
+    # one query against nine key tiles: the keys are split over a cluster
+    q, k, v = inputs(1, 1, 1100, hq, hk, d, seed=21)
+    want = forward_and_backward(q, k, v, None)
+    q[0, 0, hq - 1, 3] = value  # keys of either sign there: scores of +inf and -inf, or NaN
+    o, lse, dq, dk, dv = forward_and_backward(q, k, v, None)
+    assert torch.isnan(o[0, 0, hq - 1]).all() and torch.isnan(lse[0, hq - 1]).all()
+    assert torch.isnan(dq[0, 0, hq - 1]).all()
+    assert torch.isnan(dk[:, :, hk - 1]).all() and torch.isnan(dv[:, :, hk - 1]).all()
+    # the other heads are untouched
+    assert torch.equal(o[:, :, :hq - 1], want[0][:, :, :hq - 1]) and torch.equal(lse[:, :hq - 1], want[1][:, :hq - 1])
+    assert torch.equal(dq[:, :, :hq - 1], want[2][:, :, :hq - 1])
+    assert torch.equal(dk[:, :, :hk - 1], want[3][:, :, :hk - 1])
+
+
+@pytest.mark.parametrize("at", [0, 700, 1099])
+def test_a_nan_key_shows_where_keys_are_split(at):
+    q, k, v = inputs(1, 1, 1100, 2, 2, 64, seed=22)
+    k[0, at, 1, 5] = float("nan")
+    o, lse = pa.masked_attention(q, k, v, want_lse=True)
+    assert torch.isfinite(o[:, :, 0]).all() and torch.isnan(o[:, :, 1]).all() and torch.isnan(lse[:, 1]).all()
+
+
+def test_parts_of_split_keys_that_see_nothing():
+    # documents of a single key tile: the other parts of the cluster hold nothing and say so
+    q, k, v = inputs(1, 1, 1100, 2, 2, 64, seed=23)
+    doc_k = torch.full((1, 1100), 3, device="cuda", dtype=torch.int32)
+    doc_k[0, 600:640] = 0
+    check(q, k, v, pa.ScoreRule(doc_q=torch.zeros(1, 1, device="cuda", dtype=torch.int32), doc_k=doc_k))
+    q[0, 0, 1, 0] = float("nan")
+    o, lse = pa.masked_attention(q, k, v, pa.ScoreRule(doc_q=torch.zeros(1, 1, device="cuda", dtype=torch.int32),
+                                                       doc_k=doc_k), want_lse=True)
+    assert torch.isfinite(o[:, :, 0]).all() and torch.isnan(o[:, :, 1]).all() and torch.isnan(lse[:, 1]).all()
+    o, lse = pa.masked_attention(q, k, v, pa.ScoreRule(doc_q=torch.ones(1, 1, device="cuda", dtype=torch.int32),
+                                                       doc_k=doc_k), want_lse=True)
+    assert not o.any() and torch.isneginf(lse).all()  # it sees no key, whatever it holds
