@@ -224,11 +224,13 @@ __device__ __forceinline__ void class_tiles(const int* ids, int count, int j0, i
 // ------------------------------------------------------------------ scores
 
 // A raw product q.k to a score in log2 units: capped, then lowered by the distance.
-//   cap:  cap tanh(y), y = scale qk / cap.  Where all |y| of a warp's 64 columns are at most 1/2
-//         (scores up to half the cap), tanh comes from y (a0 + a1 y^2 + a2 y^4 + a3 y^6), fitted for
-//         least absolute error (1.3e-7, Lawson's iteratively reweighted least squares), on pairs
-//         on the FMA pipe; else from 1 - 2 / (1 + exp(2 y)) on the special-function unit, whose
-//         absolute error is about 2^-22.  The exponential afterwards feels cap times that.
+//   cap:  cap tanh(y), y = scale qk / cap.  Where |y| is at most 1/2 (scores up to half the cap),
+//         tanh comes from y (a0 + a1 y^2 + a2 y^4 + a3 y^6), fitted for least absolute error
+//         (1.3e-7, Lawson's iteratively reweighted least squares), on pairs on the FMA pipe; else
+//         from 1 - 2 / (1 + exp(2 y)) on the special-function unit, whose absolute error is
+//         about 2^-22.  The exponential afterwards feels cap times that.  The form goes by the element
+//         alone: a warp only skips the second one where none of its elements needs it, so a
+//         row's bits depend neither on its neighbours nor on what hidden keys and unwritten rows hold.
 //   bias: -slope |position - key|.  With e = (first column's distance, signed), the 64 columns
 //         are at |e + k|; where every row of the warp lies on one side of them that is linear in
 //         k, and the row's part goes into the exponential's reference.
@@ -250,11 +252,13 @@ __device__ __forceinline__ float abs_max(const uint32_t (&s)[N]) {
   return max3_nan(mv[0], mv[1], max3_nan(mv[2], mv[3], mv[3]));
 }
 
-// Raw products to factor tanh(scale qk / cap), in place; the whole warp takes one way.
+// Raw products to factor tanh(scale qk / cap), in place.  The polynomial's steps are the same, rounding for
+// rounding, on pairs and one by one; one by one where both forms are needed (2 x 16 heads x 4216 of 72
+// with cap, bias and prefix, scores beyond half the cap in most warps: 389 us, on pairs 430).  The
+// factor's products stand in both branches: shared, they cost the first 5% (283 for 271 us).
 template <int N>
 __device__ __forceinline__ void tanh_scores(uint32_t (&s)[N], const MaskParams& m, float factor) {
-  const bool small = abs_max<N>(s) <= m.cap_half;
-  if (__all_sync(0xffffffffu, small)) {
+  if (__all_sync(0xffffffffu, abs_max<N>(s) <= m.cap_half)) {
     const float t0 = kTanh0 * factor, t1 = kTanh1 * factor, t2 = kTanh2 * factor, t3 = kTanh3 * factor;
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
@@ -267,9 +271,15 @@ __device__ __forceinline__ void tanh_scores(uint32_t (&s)[N], const MaskParams& 
       s[k + 1] = __float_as_uint(p.y);
     }
   } else {
+    const float t0 = kTanh0 * factor, t1 = kTanh1 * factor, t2 = kTanh2 * factor, t3 = kTanh3 * factor;
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      s[k] = __float_as_uint(fmaf(-2.f * factor, rcp(ex2(__uint_as_float(s[k]) * (2.f * kLog2e * m.cap_in)) + 1.f), factor));
+    for (int k = 0; k < N; ++k) {
+      const float raw = __uint_as_float(s[k]);
+      const float y = __fmul_rn(raw, m.cap_in), z = __fmul_rn(y, y);
+      const float p = __fmul_rn(__fmaf_rn(__fmaf_rn(__fmaf_rn(z, t3, t2), z, t1), z, t0), y);
+      const float e = fmaf(-2.f * factor, rcp(ex2(raw * (2.f * kLog2e * m.cap_in)) + 1.f), factor);
+      s[k] = __float_as_uint(fabsf(raw) <= m.cap_half ? p : e);
+    }
   }
 }
 

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import patch_attention_b200 as pa
-from tests.test_gpu_masked_attention import BF, check, inputs
+from tests.test_gpu_masked_attention import BF, check, documents, inputs, slopes
 from tests.test_gpu_masked_attention_bwd import check as check_bwd
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +74,52 @@ def test_parts_of_split_keys_that_see_nothing():
     o, lse = pa.masked_attention(q, k, v, pa.ScoreRule(doc_q=torch.ones(1, 1, device="cuda", dtype=torch.int32),
                                                        doc_k=doc_k), want_lse=True)
     assert not o.any() and torch.isneginf(lse).all()  # it sees no key, whatever it holds
+
+
+@pytest.mark.parametrize("d", [64, 72, 128])
+@pytest.mark.parametrize("bias", [False, True])
+def test_a_capped_row_does_not_depend_on_its_neighbours(d, bias):
+    # the cap's two forms are chosen element by element: rows beyond half the cap change no other row's bits
+    q, k, v = inputs(1, 200, 300, 2, 2, d, seed=24)
+    rule = pa.ScoreRule(softcap=20.0, slopes=slopes(2) if bias else None)
+    want = forward_and_backward(q, k, v, rule)
+    q2 = q.clone()
+    q2[:, 40:60] *= 30
+    got = forward_and_backward(q2, k, v, rule)
+    keep = [i for i in range(200) if not 40 <= i < 60]
+    assert torch.equal(got[0][:, keep], want[0][:, keep]) and torch.equal(got[1][:, :, keep], want[1][:, :, keep])
+    assert torch.equal(got[2][:, keep], want[2][:, keep])
+    assert not torch.equal(got[0][:, 40:60], want[0][:, 40:60])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 1e4])
+@pytest.mark.parametrize("d", [64, 72, 128])
+def test_unseen_keys_under_a_cap_may_hold_anything(value, d):
+    q, k, v = inputs(1, 300, 300, 2, 1, d, seed=25)
+    doc = documents(1, 300, seed=5)
+    dk = doc.clone()
+    dk[0, 130:140] = 4
+    doc[doc == 4] = 5
+    for causal in (False, True):
+        rule = pa.ScoreRule(softcap=20.0, slopes=slopes(2), causal=causal, doc_q=doc, doc_k=dk)
+        want = forward_and_backward(q, k, v, rule)
+        unseen = (dk < 0) | (dk == 4)
+        k2, v2 = k.clone(), v.clone()
+        k2[unseen] = value
+        v2[unseen] = value
+        assert same(forward_and_backward(q, k2, v2, rule), want)
+
+
+@pytest.mark.parametrize("hq,d", [(3, 64), (5, 64), (3, 72), (7, 128)])
+def test_a_capped_tile_with_unwritten_rows_repeats_its_bits(hq, d):
+    # heads that share a key head and do not divide 128 leave the last rows of a query tile unwritten; the calls in
+    # between leave large and small numbers in shared memory there
+    q, k, v = inputs(1, 200, 300, hq, 1, d, seed=26)
+    rule = pa.ScoreRule(softcap=20.0)
+    f = inputs(1, 128, 128, 160, 160, d, seed=27)
+    got = []
+    for size in (0.0, 1e3):
+        pa.masked_attention((f[0].float() * size).to(BF), f[1], f[2], rule)
+        got.append(pa.masked_attention(q, k, v, rule, want_lse=True))
+    check(q, k, v, rule)
+    assert same(*got)
