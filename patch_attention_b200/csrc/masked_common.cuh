@@ -225,18 +225,20 @@ __device__ __forceinline__ void class_tiles(const int* ids, int count, int j0, i
 
 // A raw product q.k to a score in log2 units: capped, then lowered by the distance.
 //   cap:  cap tanh(y), y = scale qk / cap.  Where |y| is at most 1/2 (scores up to half the cap),
-//         tanh comes from y (a0 + a1 y^2 + a2 y^4 + a3 y^6), fitted for least absolute error
-//         (1.3e-7, Lawson's iteratively reweighted least squares), on pairs on the FMA pipe; else
+//         tanh comes from y (a0 + a1 y^2 + a2 y^4 + a3 y^6), fitted for least relative error
+//         (5.6e-7, Lawson's iteratively reweighted least squares), on pairs on the FMA pipe; else
 //         from 1 - 2 / (1 + exp(2 y)) on the special-function unit, whose absolute error is
-//         about 2^-22.  The exponential afterwards feels cap times that.  The form goes by the element
-//         alone: a warp only skips the second one where none of its elements needs it, so a
-//         row's bits depend neither on its neighbours nor on what hidden keys and unwritten rows hold.
+//         about 2^-22.  So a capped score is off by about 2^-20 of itself, however large the cap
+//         (the fit for least absolute error, 1.3e-7, was off by 2.3e-6 of a score far below the cap).
+//         The form goes by the element alone: a warp only skips the second one where none of its
+//         elements needs it, so a row's bits depend neither on its neighbours nor on what hidden
+//         keys and unwritten rows hold.
 //   bias: -slope |position - key|.  With e = (first column's distance, signed), the 64 columns
 //         are at |e + k|; where every row of the warp lies on one side of them that is linear in
 //         k, and the row's part goes into the exponential's reference.
 // (One special-function result per element for the softmax and two for the exact tanh: they
 // bound a capped tile of 128 x 128 at three times 1024 cycles, the polynomial at about 1100.)
-constexpr float kTanh0 = 0.99999768f, kTanh1 = -0.33320656f, kTanh2 = 0.13145144f, kTanh3 = -0.043372445f;
+constexpr float kTanh0 = 0.999999464f, kTanh1 = -0.333263189f, kTanh2 = 0.131903037f, kTanh3 = -0.044402387f;
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 

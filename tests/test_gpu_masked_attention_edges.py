@@ -1,10 +1,13 @@
 """Masked attention at the ends of its arguments' ranges.  Tolerances as in the forward and backward tests, or equal
 bits."""
+import numpy as np
 import pytest
 import torch
 
 import patch_attention_b200 as pa
-from tests.test_gpu_masked_attention import BF, check, documents, inputs, slopes
+from tests._bounds import within
+from tests._oracle_util import f64
+from tests.test_gpu_masked_attention import BF, E, check, documents, inputs, slopes
 from tests.test_gpu_masked_attention_bwd import check as check_bwd
 
 pytestmark = pytest.mark.gpu
@@ -123,3 +126,32 @@ def test_a_capped_tile_with_unwritten_rows_repeats_its_bits(hq, d):
         got.append(pa.masked_attention(q, k, v, rule, want_lse=True))
     check(q, k, v, rule)
     assert same(*got)
+
+
+@pytest.mark.parametrize("cap", [1.0, 30.0, 1e4, 1e6])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_the_cap_is_exact_far_below_it(cap, mixed):
+    """With one key and one non-zero column the score is a product of two bf16 numbers, exact in fp32, and lse is the
+    capped score w.  With y = s / cap: the polynomial (|y| <= 1/2) is within 9.3 E (5.6e-7) of tanh relative to it,
+    scale / cap, y, y^2, three steps, the last product, the factor and its log2(e) round once each (10 E), the
+    reference and lse twice more (3 E): 24 E |w|.  Beyond, 1 - 2 / (1 + exp(2 y)): the argument rounds three times
+    (relative 3 E of 2 y: 6 E y exp(2 y) in exp(2 y), at most 1.4 E after division), the exponential and the
+    reciprocal are approximate by 4 E each, the difference and the factor as above: 16 E cap + 6 E |w|."""
+    g = torch.Generator(device="cuda").manual_seed(28)
+    n = 256
+    frac = torch.rand(n, device="cuda", generator=g) * 0.49 * torch.where(torch.arange(n, device="cuda") % 2 == 0, 1.0, -1.0)
+    frac[::3] *= 1e-3
+    frac[::7] *= 1e-5
+    if mixed:  # every fifth row beyond half the cap
+        frac[::5] = 0.6 + 3.0 * torch.rand(frac[::5].shape, device="cuda", generator=g)
+    q = torch.zeros(1, n, 1, 64, device="cuda", dtype=BF)
+    q[0, :, 0, 0] = (frac * cap).to(BF)
+    k = torch.zeros(1, 1, 1, 64, device="cuda", dtype=BF)
+    k[..., 0] = 1.0
+    v = torch.ones_like(k)
+    o, lse = pa.masked_attention(q, k, v, pa.ScoreRule(softcap=cap, softmax_scale=1.0), want_lse=True)
+    s = f64(q[0, :, 0, 0])
+    w = cap * np.tanh(s / cap)
+    bound = np.where(np.abs(s) <= 0.5 * cap, 24 * E * np.abs(w), 16 * E * cap + 6 * E * np.abs(w))
+    within(f64(lse[0, 0]), w, bound, "lse")
+    assert (o == 1.0).all()
