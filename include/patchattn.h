@@ -273,7 +273,7 @@ typedef struct {
   int head_dim;        /* 64, 72 or 128 */
   int n_q, n_k;        /* >= 0, at most 2^30; with documents n_k is at most 2^20 */
   float softmax_scale; /* 0 => 1/sqrt(head_dim) */
-  float softcap;       /* 0 => none; a capped score is within about 2^-20 of itself */
+  float softcap;       /* 0 => none, else at most 1e30 softmax_scale; a capped score is within about 2^-20 of itself */
   int causal;
   pf_strides q, k, v;  /* element strides, positive multiples of 8 (where the extent is above 1) */
 } pf_masked_attn_config;

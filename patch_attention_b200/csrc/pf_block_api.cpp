@@ -143,6 +143,8 @@ pf_status check_masked(const pf_masked_attn_config* c) {
   if (!(c->softcap >= 0.f) || !std::isfinite(c->softcap * kLog2e) || !std::isfinite(scale_of(*c) * kLog2e) ||
       !std::isfinite(3.f * cap_in_of(*c)))
     return PF_ERR_INVALID_ARG;
+  // products are divided by cap / scale, in 32 bits: below this the quotients would lose bits or vanish
+  if (c->softcap > 0.f && cap_in_of(*c) < 1e-30f) return PF_ERR_INVALID_ARG;
   // CTAs (at most 8 per query tile and head, or per key tile) on a 31-bit grid
   const double longest = c->n_q > c->n_k ? c->n_q : c->n_k;
   if (static_cast<double>(c->batch) * c->heads_q * (longest / 128 + 1) * 8 > 2147483647.0) return PF_ERR_SHAPE;
