@@ -81,6 +81,13 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _kept_in_32_bits(x: float, name: str) -> float:
+    """x, refused where the C ABI's float would be 0, which stands for a default or for none, and x is not."""
+    if x != 0 and ctypes.c_float(x).value == 0:
+        raise ValueError(f"{name} of {x} is 0 in 32 bits")
+    return x
+
+
 def _layout(t: Optional[torch.Tensor]):
     return None if t is None else (t.shape, t.stride(), t.dtype)
 
@@ -290,6 +297,7 @@ def _rope_config(q, k, pos, axes: RopeAxes, eps) -> pf_rope_config:
         raise ValueError("pos must be contiguous")
     if eps is not None and not eps > 0:
         raise ValueError("eps must be positive (None: no norm)")
+    _kept_in_32_bits(eps or 0.0, "eps")
     pad = (0,) * (4 - na)
     return pf_rope_config(b, n, 0 if q is None else q.shape[2], 0 if k is None else k.shape[2], d, na,
                           (ctypes.c_int * 4)(*(axes.dims + pad)), (ctypes.c_double * 4)(*(axes.theta + pad)),
@@ -441,6 +449,8 @@ class ScoreRule:
 
 def _masked_config(q, k, v, scale, cap, causal):
     """(reference to the configuration, shapes of lse, slopes, prefix, doc_q, doc_k)."""
+    _kept_in_32_bits(scale, "softmax_scale")
+    _kept_in_32_bits(cap, "softcap")
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if t.dim() != 4:
             raise ValueError(f"{name} must be [batch, tokens, heads, head_dim], got {tuple(t.shape)}")
