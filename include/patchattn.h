@@ -309,7 +309,8 @@ pf_status pf_masked_attn_bwd(const pf_masked_attn_config* cfg, const void* dout,
                              const int32_t* doc_k, void* dq, void* dk, void* dv, void* workspace,
                              size_t workspace_bytes, void* stream);
 
-/* pf_check_device_status for operators that have no context. */
+/* pf_check_device_status for operators that have no context: of the current device, to which the
+ * stream has to belong. */
 pf_status pf_device_status(void* stream);
 
 /* Bytes of the optional attention workspace for this configuration (0 if cfg is invalid, or

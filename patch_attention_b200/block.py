@@ -492,12 +492,17 @@ def pf_masked_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.T
                                  _raw_stream(i)), "pf_masked_attn")
 
 
-def pf_device_status(stream=None) -> None:
-    """Synchronise the stream; raises if a kernel's bounded wait expired on this device."""
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    _check(_lib().pf_device_status(raw), "pf_device_status")
+def pf_device_status(stream=None, device=None) -> None:
+    """Synchronise the stream; raises if a kernel's bounded wait expired on its device, and clears that report.  The
+    device is the stream's; ``device`` names it for a raw handle or for the current stream of another device (default:
+    the current device)."""
+    if isinstance(stream, torch.cuda.Stream):
+        if device is not None and device not in (stream.device, stream.device.index, str(stream.device)):
+            raise ValueError(f"the stream belongs to {stream.device}, not {device}")
+        device, stream = stream.device, stream.cuda_stream
+    with torch.cuda.device(device):  # the status word is the current device's
+        raw = torch.cuda.current_stream().cuda_stream if stream is None else int(stream)
+        _check(_lib().pf_device_status(raw), "pf_device_status")
 
 
 def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rule: Optional[ScoreRule] = None, *,

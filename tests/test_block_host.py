@@ -1,4 +1,7 @@
 """Host side of the block operators at the ends of their arguments' ranges; no GPU is needed."""
+import contextlib
+import types
+
 import pytest
 import torch
 
@@ -34,3 +37,62 @@ def test_a_number_that_is_zero_in_32_bits_is_not_taken_for_none():
         with pytest.raises(ValueError):
             block._masked_config(q, q, q, scale, cap, False)
     block._masked_config(q, q, q, 0.0, 0.0, False)
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    """Two fake devices with a status word each; pf_device_status reads and clears the current one's."""
+    at = types.SimpleNamespace(current=0, words=[0, 0], synchronised=[])
+
+    class Stream:
+        def __init__(self, index, handle):
+            self.device, self.cuda_stream = torch.device("cuda", index), handle
+
+    @contextlib.contextmanager
+    def device(d):
+        before = at.current
+        if d is not None:
+            at.current = d if isinstance(d, int) else torch.device(d).index
+        try:
+            yield
+        finally:
+            at.current = before
+
+    class Lib:
+        @staticmethod
+        def pf_device_status(raw):
+            at.synchronised.append(raw)
+            word, at.words[at.current] = at.words[at.current], 0
+            return pa.PF_ERR_TIMEOUT if word else pa.PF_OK
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream(at.current, 100 + at.current))
+    monkeypatch.setattr(block, "_lib", lambda: Lib)
+    at.stream = Stream
+    return at
+
+
+def test_the_device_status_is_that_of_the_streams_device(two_devices):
+    at = two_devices
+    at.words[1] = 4
+    block.pf_device_status()  # device 0 has nothing to report, and device 1's report stays
+    block.pf_device_status(at.stream(0, 7))
+    assert at.words == [0, 4] and at.synchronised == [100, 7]
+    with pytest.raises(pa.PatchAttnError) as e:
+        block.pf_device_status(at.stream(1, 8))
+    assert e.value.status == pa.PF_ERR_TIMEOUT and at.current == 0 and at.words == [0, 0]
+    block.pf_device_status(at.stream(1, 8))  # the report is cleared
+    assert at.synchronised == [100, 7, 8, 8]
+
+
+def test_the_device_status_of_a_named_device(two_devices):
+    at = two_devices
+    for stream, raw in ((None, 101), (9, 9), (0, 0)):
+        at.words = [0, 2]
+        block.pf_device_status(stream)
+        with pytest.raises(pa.PatchAttnError):
+            block.pf_device_status(stream, device=1)
+        assert at.synchronised[-1] == raw and at.current == 0 and at.words == [0, 0]
+    with pytest.raises(ValueError):
+        block.pf_device_status(at.stream(1, 8), device="cuda:0")
