@@ -15,6 +15,7 @@ structures they lead to, so that a call of a layout seen before costs little mor
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -24,6 +25,7 @@ from . import PF_BF16, PF_F16, PF_F32, _check, _lib, pf_masked_attn_config, pf_r
 _DTYPES = {torch.bfloat16: PF_BF16, torch.float16: PF_F16, torch.float32: PF_F32}
 _BF, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _MOST_LAYOUTS = 4096
+_keeping = threading.Lock()
 
 
 def _index(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
@@ -93,13 +95,15 @@ def _layout(t: Optional[torch.Tensor]):
 
 
 def _kept(plans: dict, key, make):
-    """plans[key], made on first use; the oldest layouts go when there are too many."""
+    """plans[key], made on first use; the oldest layouts go when there are too many.  Threads may ask at once: what is
+    there is read without the lock, two that make the same plan keep one of them."""
     plan = plans.get(key)
     if plan is None:
         plan = make()
-        while len(plans) >= _MOST_LAYOUTS:
-            plans.pop(next(iter(plans)), None)
-        plans[key] = plan
+        with _keeping:
+            while len(plans) >= _MOST_LAYOUTS:
+                plans.pop(next(iter(plans)), None)
+            plans[key] = plan
     return plan
 
 

@@ -1,5 +1,7 @@
 """Host side of the block operators at the ends of their arguments' ranges; no GPU is needed."""
 import contextlib
+import sys
+import threading
 import types
 
 import pytest
@@ -96,3 +98,28 @@ def test_the_device_status_of_a_named_device(two_devices):
         assert at.synchronised[-1] == raw and at.current == 0 and at.words == [0, 0]
     with pytest.raises(ValueError):
         block.pf_device_status(at.stream(1, 8), device="cuda:0")
+
+
+def test_many_threads_with_layouts_of_their_own(monkeypatch):
+    monkeypatch.setattr(block, "_MOST_LAYOUTS", 8)
+    plans, errors = {}, []
+
+    def work(t):
+        try:
+            for i in range(3000):
+                key = (t, i) if i % 3 else i % 5  # own layouts and shared ones
+                assert block._kept(plans, key, lambda: ("plan", key)) == ("plan", key)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    every = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=work, args=(t,)) for t in range(8)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(every)
+    assert not errors and len(plans) == 8
