@@ -53,7 +53,7 @@ pf_status make_rope(const pf_rope_config* c, pf::RopeArgs& a) {
   if (!dtype_ok(c->dtype)) return PF_ERR_UNSUPPORTED;
   if (!(c->eps >= 0.f) || std::isinf(c->eps)) return PF_ERR_INVALID_ARG;
   if (c->pos_batch_stride < 0) return PF_ERR_INVALID_ARG;
-  // items (tokens times head shares) are counted in blocks of 8 warps on a 31-bit grid
+  // a block takes one to four tokens, on a 31-bit grid
   if (static_cast<int64_t>(c->batch) * c->tokens > INT32_MAX) return PF_ERR_SHAPE;
   std::memset(&a, 0, sizeof(a));
   a.batch = c->batch;

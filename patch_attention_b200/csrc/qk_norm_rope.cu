@@ -489,7 +489,8 @@ Grid grid_of(const RopeParams& p, bool bwd) {
   const int chunks = p.head_dim / 8;
   const int per_step = chunks <= 4 ? 8 : chunks <= 8 ? 4 : chunks <= 16 ? 2 : 1;  // vectors of a warp at once
   const long long steps = (p.heads[0] + p.heads[1] + per_step - 1) / per_step;    // most warps with work
-  const long long want = (148 * 64 + p.total - 1) / p.total;
+  const long long total = p.total;  // up to 2^31 - 1: sums in 64 bits
+  const long long want = (148 * 64 + total - 1) / total;
   Grid g = {1, 1, 0};
   while (g.shares < kWarps && g.shares < want && g.shares < steps) g.shares *= 2;
   if (!bwd && g.shares == kWarps) {
@@ -497,7 +498,7 @@ Grid grid_of(const RopeParams& p, bool bwd) {
     g.splits = static_cast<int>((more + kWarps - 1) / kWarps);
   }
   const int per_block = kWarps / g.shares;
-  g.blocks = (p.total + per_block - 1) / per_block;
+  g.blocks = static_cast<int>((total + per_block - 1) / per_block);
   // backward: the blocks that are resident at once walk the tokens, so that few partial gain
   // gradients are written
   if (bwd && g.blocks > 148 * 4) g.blocks = 148 * 4;

@@ -9,7 +9,7 @@ import torch
 
 import patch_attention_b200 as pa
 from patch_attention_b200 import block
-from tests.test_block_args import _attn, _attn_bwd, _attn_cfg
+from tests.test_block_args import _attn, _attn_bwd, _attn_cfg, _rope_cfg
 
 
 @pytest.mark.parametrize("cap,scale", [(1e30, 0.0), (3e38, 0.0), (1e25, 1e-6), (1e30, 0.9), (100.0, 1e-29)])
@@ -24,6 +24,16 @@ def test_a_cap_beyond_what_32_bits_divide_by_is_refused(cap, scale):
 def test_large_and_small_caps_are_taken(cap, scale):
     assert pa.pf_masked_attn_bwd_workspace_bytes(_attn_cfg(softcap=cap, softmax_scale=scale)) > 0
     assert _attn(_attn_cfg(softcap=cap, softmax_scale=scale, n_q=0), q=None, o=None) == pa.PF_OK
+
+
+@pytest.mark.parametrize("less", [0, 1, 2, 3, 4, 5000, 9471, 9472, 20000])
+@pytest.mark.parametrize("head_dim", [64, 256])
+def test_rotary_sizes_up_to_the_most_tokens(less, head_dim):
+    # as many partial rows as for any long call: what is resident at once
+    axes = dict(head_dim=head_dim, n_axes=1, axis_dim=(head_dim,), theta=(1e4,))
+    want = pa.pf_qk_norm_rope_bwd_workspace_bytes(_rope_cfg(tokens=1 << 20, **axes))
+    assert want > 0
+    assert pa.pf_qk_norm_rope_bwd_workspace_bytes(_rope_cfg(tokens=2 ** 31 - 1 - less, **axes)) == want
 
 
 def test_a_number_that_is_zero_in_32_bits_is_not_taken_for_none():
