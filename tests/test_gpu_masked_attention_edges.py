@@ -42,7 +42,7 @@ def test_a_prefix_below_zero_is_none(prefix, nq, nk, d):
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("hq,hk,d", [(1, 1, 64), (2, 2, 72), (6, 2, 128)])
 def test_a_nan_or_infinite_score_shows_where_keys_are_split(value, hq, hk, d):
-    # one query against nine key tiles: the keys are split over a cluster
+    # one query against nine key tiles: the keys are split over a cluster (tests/test_masked_plan_host.py)
     q, k, v = inputs(1, 1, 1100, hq, hk, d, seed=21)
     want = forward_and_backward(q, k, v, None)
     q[0, 0, hq - 1, 3] = value  # keys of either sign there: scores of +inf and -inf, or NaN
