@@ -522,7 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_fwd_kernel(const __grid_co
       ++n;
     }
     if (!ok && lane == 0) raise_abort(abort, p.watchdog, kWdSoftmax);
-    bool ok_o = ok && mbar_wait(smem_u32(o_full + t), 0, abort, kWaitNs);
+    // (a tile without work has no O to wait for: the wait would last as long as the other tile's work)
+    bool ok_o = ok && (n == 0 || mbar_wait(smem_u32(o_full + t), 0, abort, kWaitNs));
     ok_o = named_bar_and(1 + t, kRows, ok_o);
     if (!ok_o) {
       if (ok && lane == 0) raise_abort(abort, p.watchdog, kWdEpilogue);
