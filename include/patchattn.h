@@ -265,7 +265,8 @@ pf_status pf_qk_norm_rope_bwd(const pf_rope_config* cfg, const float* pos, const
  *   given) and, where documents are given, doc_q[i] = doc_k[j] >= 0 (a negative id is padding)
  *   o_i = sum over visible j of softmax_j(s_ij) v_j; a query that sees no key gives 0
  * Keys and values that no query sees may hold anything (padding, unwritten cache rows); those that
- * some query sees should be finite, as a value reaches its whole tile of 128 rows. */
+ * some query sees should be finite, as a value reaches its whole tile of 128 rows.  A query with a
+ * NaN score or one of +inf gives NaN (o and lse); one whose scores are all -inf counts as seeing no key. */
 typedef struct {
   int batch;           /* >= 1 */
   int heads_q;         /* >= 1, a multiple of heads_kv: query head h uses key head h * heads_kv / heads_q */

@@ -436,7 +436,7 @@ _attn_plans: dict = {}
 
 class ScoreRule:
     """What attention does to its scores before the softmax: ``softmax_scale`` (0: 1/sqrt(head_dim)), a cap
-    ``softcap * tanh(s / softcap)`` (0: none), a distance bias ``-slopes[head] * |position - key|``, and which keys a
+    ``softcap * tanh(s / softcap)`` (0: none; at most 1e30 times the scale), a distance bias ``-slopes[head] * |position - key|``, and which keys a
     query sees: all, or with ``causal`` those up to its position (queries are the last positions) and those before
     ``prefix[batch]``; and, with ``doc_q`` and ``doc_k`` (int32 ids, negative: padding), only keys of its document."""
 
@@ -551,8 +551,8 @@ def pf_masked_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
 
 def masked_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                               lse: torch.Tensor, rule: Optional[ScoreRule] = None, *, stream=None):
-    """(dq, dk, dv) of ``masked_attention`` from the gradient of its output, its inputs, and the o and lse that it
-    returned; contiguous, dk and dv summed over the query heads that share a key head."""
+    """(dq, dk, dv) of ``masked_attention`` from the gradient of its output (contiguous, as o), its inputs, and the o and
+    lse that it returned; contiguous, dk and dv summed over the query heads that share a key head."""
     i = _index(q)
     if _elsewhere(i, stream):
         with _on(i, stream):

@@ -4,6 +4,7 @@
 //   key j is visible to query i if (not causal, or j <= p_i, or j < prefix) and, with documents,
 //   doc_q[i] = doc_k[j] >= 0
 //   o_i = sum_j softmax_j(s_ij) v_j over the visible keys; a query that sees none gives 0
+// P is rounded to bf16, the type that the matrix product takes; sums, maxima and O are fp32.
 //
 // One CTA handles NQ (1 or 2) tiles of 128 query rows against a run of 128-key tiles, by the
 // split-tile scheme of the patch attention: each key tile is two 64-key halves with their own
@@ -19,13 +20,14 @@
 // shared memory -- no workspace, no counters, and the same order of sums every time.
 //
 // What bounds it, measured on a B200: at head_dim 128 the tensor core (24 heads x 16538 x 16538:
-// 2.62 ms, 1280 TFLOP/s); at head_dim 64 the softmax warps, two per scheduler in step with each
-// other -- of 1600 cycles per 128 x 128 tile 1024 are the special-function unit's, the rest is the
-// maximum, the TMEM copies and the hand-over (2.30 ms, 730 TFLOP/s; three packed documents 1.17 ms).
-// A cap adds 1000 cycles per tile and a bias 800 (2 x 16 x 4216, head_dim 72, causal: 145 us without,
-// 270 us with cap, bias and prefix).  Documents that end inside tiles cost the query tiles that meet
-// two of them the keys of both.  One token against 8 x 16538 keys (24 / 8 heads of 128): 108 us,
-// 5.0 TB/s of K and V.
+// 2.56 to 2.81 ms by the power left, 1200 to 1310 TFLOP/s); at head_dim 64 the softmax warps, two
+// per scheduler in step with each other -- of 1600 cycles per 128 x 128 tile 1024 are the
+// special-function unit's, the rest is the maximum, the TMEM copies and the hand-over (2.32 ms,
+// 725 TFLOP/s; three packed documents 1.17 ms).  A cap adds 1000 cycles per tile and a bias 800
+// (2 x 16 x 4216, head_dim 72, causal: 142 us without, 271 us with cap, bias and prefix by itself and
+// 296 among other calls, 389 where scores pass half the cap).  Documents that end inside tiles
+// cost the query tiles that meet two of them the keys of both.  One token against 8 x 16538 keys
+// (24 / 8 heads of 128): 108 us by itself, 116 among other calls, 5.0 and 4.7 TB/s of K and V.
 //
 // A value row that no query of the CTA sees may hold anything (padding, unwritten cache rows):
 // its products with the zero probabilities would still be NaN, so a warp zeroes such rows in

@@ -24,12 +24,14 @@
 // columns wide (64 at N = 128) and not per warpgroup (84 measured at N = 64, where 32 would do).  The
 // two halves of a streaming tile are loaded and freed apart: two whole tiles fill the shared
 // memory at head_dim 128, and half a tile's start is gained for the loads.  P and dS are rounded to
-// bf16, the operand type; everything else is fp32.
+// bf16, the operand type, and delta is summed from the bf16 o that the forward call wrote;
+// everything else is fp32.  So dq and dk are off by 1.45 times as much as with all three in fp32 where
+// a query sees 32 keys or more, by 2.4 times at two keys, where do.v and delta nearly cancel.
 //
 // What bounds it, measured on a B200: the chain of a tile through the softmax warps (per 128 x 128
 // tile 2000 to 2900 cycles at head_dim 64, 3000 to 4100 at 128, where the loads also come late; the
-// exponentials are 1024 of them).  24 heads x 16538 x 16538: 7.57 ms at head_dim 64, 12.0 ms at 128
-// (555 and 680 TFLOP/s of the five products' work); 4216 tokens in two documents, 24 / 8 heads of
+// exponentials are 1024 of them).  24 heads x 16538 x 16538: 7.50 ms at head_dim 64, 11.7 ms at 128
+// (560 and 720 TFLOP/s of the five products' work); 4216 tokens in two documents, 24 / 8 heads of
 // 128: 622 us.  The grid of dQ starts while that of dK, dV still runs and fills the SMs that its
 // last CTAs leave idle: one after the other the same call took 775 us.
 //
