@@ -436,9 +436,10 @@ _attn_plans: dict = {}
 
 class ScoreRule:
     """What attention does to its scores before the softmax: ``softmax_scale`` (0: 1/sqrt(head_dim)), a cap
-    ``softcap * tanh(s / softcap)`` (0: none; at most 1e30 times the scale), a distance bias ``-slopes[head] * |position - key|``, and which keys a
-    query sees: all, or with ``causal`` those up to its position (queries are the last positions) and those before
-    ``prefix[batch]``; and, with ``doc_q`` and ``doc_k`` (int32 ids, negative: padding), only keys of its document."""
+    ``softcap * tanh(s / softcap)`` (0: none; at most 1e30 times the scale), a distance bias
+    ``-slopes[head] * |position - key|``, and which keys a query sees: all, or with ``causal`` those up to its position
+    (queries are the last positions) and those before ``prefix[batch]`` (zero and below: none); and, with ``doc_q`` and
+    ``doc_k`` (int32 ids, negative: padding), only keys of its document."""
 
     def __init__(self, softmax_scale: float = 0.0, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
                  causal: bool = False, prefix: Optional[torch.Tensor] = None, doc_q: Optional[torch.Tensor] = None,
